@@ -46,6 +46,23 @@ class _W4Matrix(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
 
 
+class _W4KvPages(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_int32), ("num_pages", ctypes.c_int64), ("Hkv", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+class _W4KvBatch(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("rows", ctypes.c_int64), ("max_rows", ctypes.c_int64),
+                ("max_len", ctypes.c_int64), ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_width", ctypes.c_int64), ("table_stride", ctypes.c_int64)]
+
+
+class _W4Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SIGS = {
@@ -65,6 +82,15 @@ _SIGS = {
                                    _P], ctypes.c_int),
     "w4_kv_weighted_sum": ([_P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, ctypes.c_size_t, _P],
                            ctypes.c_int),
+    "w4_kv_write": ([ctypes.POINTER(_W4KvPages), ctypes.POINTER(_W4KvBatch), ctypes.POINTER(_W4Rows),
+                     ctypes.POINTER(_W4Rows), _P], ctypes.c_int),
+    "w4_kv_read": ([ctypes.POINTER(_W4KvPages), ctypes.POINTER(_W4KvBatch), ctypes.POINTER(_W4Rows),
+                    ctypes.POINTER(_W4Rows), _P], ctypes.c_int),
+    "w4_kv_attention_workspace_bytes": ([ctypes.POINTER(_W4KvPages), ctypes.POINTER(_W4KvBatch), _I64, _I64,
+                                         _I64], ctypes.c_size_t),
+    "w4_kv_attention": ([ctypes.POINTER(_W4KvPages), ctypes.POINTER(_W4KvBatch), ctypes.POINTER(_W4Rows), _I64,
+                         ctypes.c_float, _I64, _I64, ctypes.POINTER(_W4Rows), _P, _P, ctypes.c_size_t, _P],
+                        ctypes.c_int),
     "w4a16_gemv_ws": ([ctypes.POINTER(_W4Matrix), _P, _I64, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "w4a16_gemv_multi": ([ctypes.POINTER(ctypes.POINTER(_W4Matrix)), ctypes.c_int, _P, _I64,
                           ctypes.POINTER(ctypes.c_void_p), _P], ctypes.c_int),
@@ -436,6 +462,169 @@ def kv_weighted_sum_append(p: torch.Tensor, v_new: torch.Tensor, codes: torch.Te
                                            _ptr(scales), _ptr(out), _ptr(workspace),
                                            workspace.numel() * workspace.element_size(), _stream(p.device)))
     return out
+
+
+# ---------------------------------------------------------------- batched INT4 KV cache
+_ROW_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+class KVPages:
+    """The pool of a batched INT4 KV cache: codes uint8 [pages][Hkv][page_size][D / 2] and scales
+    fp32 [pages][Hkv][page_size] of the keys and of the values (w4_kv_pages in include/w4a16.h).
+    The tensors are the caller's; kv_pages allocates them."""
+
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                 v_scales: torch.Tensor):
+        for t, name in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"), (v_scales, "v_scales")):
+            _dev(t, name)
+            if t.device != k_codes.device:
+                raise ValueError(f"{name} is on {t.device}, k_codes on {k_codes.device}")
+        if k_codes.dim() != 4 or k_codes.dtype != torch.uint8 or v_codes.dtype != torch.uint8:
+            raise ValueError("codes must be uint8 [pages][Hkv][page_size][D / 2]")
+        if v_codes.shape != k_codes.shape:
+            raise ValueError("k_codes and v_codes differ in shape")
+        for t in (k_scales, v_scales):
+            if t.dtype != torch.float32 or t.shape != k_codes.shape[:3]:
+                raise ValueError("scales must be float32 [pages][Hkv][page_size]")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.num_pages, self.Hkv, self.page_size = k_scales.shape
+        self.D = 2 * k_codes.shape[3]
+        self.device = k_codes.device
+        self._c = _W4KvPages(self.D, self.num_pages, self.Hkv, self.page_size, _ptr(k_codes), _ptr(k_scales),
+                             _ptr(v_codes), _ptr(v_scales))
+        self._ref = ctypes.byref(self._c)
+
+
+def kv_pages(num_pages: int, Hkv: int, page_size: int, D: int = KV_HEAD_DIM, device="cuda") -> KVPages:
+    """An empty pool of `num_pages` pages of `page_size` positions for Hkv heads of D = 64, 128 or 256."""
+    shape = (num_pages, Hkv, page_size)
+    codes = [torch.empty(shape + (D // 2,), dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.empty(shape, dtype=torch.float32, device=device) for _ in range(2)]
+    return KVPages(codes[0], scales[0], codes[1], scales[1])
+
+
+class KVBatch:
+    """Which rows and pages belong to which sequence (w4_kv_batch in include/w4a16.h).
+
+    lens int32 [B] (device): positions each sequence holds, the rows of the call included.
+    table int32 [B][width] (device) or None: the page of every page_size positions; without it
+    sequence b owns page b. starts int32 [B + 1] (device) or None: the packed rows of sequence b
+    are starts[b] .. starts[b + 1] - 1; without it every sequence has rows / B rows. rows: packed
+    rows in all (default B, one a sequence); max_rows, max_len: the most rows and positions of one
+    sequence, which shape the launch (default: as many as there can be). The device tensors are
+    read when the kernels run: a captured graph follows what they hold then."""
+
+    def __init__(self, lens: torch.Tensor, table: Optional[torch.Tensor] = None,
+                 starts: Optional[torch.Tensor] = None, rows: Optional[int] = None,
+                 max_rows: Optional[int] = None, max_len: Optional[int] = None):
+        for t, name, dim in ((lens, "lens", 1), (starts, "starts", 1), (table, "table", 2)):
+            if t is None:
+                continue
+            if t.dtype != torch.int32 or t.dim() != dim or not t.is_cuda:
+                raise ValueError(f"{name} must be an int32 device tensor of {dim} dimension(s)")
+            if t.shape[-1] > 1 and t.stride(-1) != 1:
+                raise ValueError(f"{name} must be contiguous along its last dimension")
+            if t.device != lens.device:
+                raise ValueError(f"{name} is on {t.device}, lens on {lens.device}")
+        B = lens.shape[0]
+        if starts is not None:
+            if starts.shape[0] != B + 1:
+                raise ValueError(f"starts must hold {B + 1} entries")
+            if rows is None:
+                raise ValueError("starts needs the number of packed rows")
+        if table is not None and table.shape[0] != B:
+            raise ValueError(f"table must hold {B} sequences")
+        self.lens, self.table, self.starts = lens, table, starts
+        self.B, self.rows, self.device = B, B if rows is None else int(rows), lens.device
+        width = table.shape[1] if table is not None else 0
+        stride = table.stride(0) if table is not None and B > 1 else width
+        self._c = _W4KvBatch(B, self.rows, int(max_rows or 0), int(max_len or 0), _ptr(lens), _ptr(starts),
+                             _ptr(table), width, stride)
+        self._ref = ctypes.byref(self._c)
+
+
+def _rows_desc(t: torch.Tensor, name: str, cache: KVPages, batch: KVBatch, heads: int) -> _W4Rows:
+    """w4_rows of a tensor [rows or more][heads][D]."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.D or t.shape[0] < batch.rows:
+        raise ValueError(f"{name} must be [{batch.rows} or more][{heads}][{cache.D}], not {tuple(t.shape)}")
+    code = _ROW_TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    rs, hs, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    return _W4Rows(t.data_ptr(), code, rs, hs)
+
+
+def _kv_call(cache: KVPages, batch: KVBatch, f, *args) -> None:
+    """f(*args, stream) on the cache's device."""
+    if batch.device != cache.device:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    if torch.cuda.current_device() == cache.device.index:
+        rc = f(*args, _stream(cache.device))
+    else:
+        with torch.cuda.device(cache.device):
+            rc = f(*args, _stream(cache.device))
+    _check(rc)
+
+
+def kv_write(k: Optional[torch.Tensor], v: Optional[torch.Tensor], cache: KVPages, batch: KVBatch) -> None:
+    """Quantize rows k, v (fp32 or bf16 [rows][Hkv][D], strided; either may be None) into the cache at
+    each sequence's last positions."""
+    d = [None if t is None else _rows_desc(t, n, cache, batch, cache.Hkv) for t, n in ((k, "k"), (v, "v"))]
+    _kv_call(cache, batch, lib().w4_kv_write, cache._ref, batch._ref, *d)
+
+
+def kv_read(cache: KVPages, batch: KVBatch, dtype: torch.dtype = torch.bfloat16,
+            k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None):
+    """The keys and values of the batch's rows read back from the cache: (k, v) [rows][Hkv][D], into the
+    given tensors, or into new ones of `dtype` if neither is given (with one given, only that one)."""
+    if k is None and v is None:
+        shape = (batch.rows, cache.Hkv, cache.D)
+        k, v = (torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+    d = [None if t is None else _rows_desc(t, n, cache, batch, cache.Hkv) for t, n in ((k, "k"), (v, "v"))]
+    _kv_call(cache, batch, lib().w4_kv_read, cache._ref, batch._ref, *d)
+    return k, v
+
+
+def kv_attention_workspace(cache: KVPages, batch: KVBatch, Hq: int, window: int = 0,
+                           sinks: int = 0) -> Optional[torch.Tensor]:
+    """A workspace for kv_attention with these sizes (None where it needs none)."""
+    n = int(lib().w4_kv_attention_workspace_bytes(cache._ref, batch._ref, Hq, window, sinks))
+    return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+
+
+def kv_attention(q: torch.Tensor, cache: KVPages, batch: KVBatch, scale: Optional[float] = None,
+                 window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,
+                 lse: Optional[torch.Tensor] = None, want_lse: bool = False,
+                 workspace: Optional[torch.Tensor] = None):
+    """Causal attention of the batch's rows q (fp32 or bf16 [rows][Hq][D], strided) over their sequences'
+    cached positions, with window > 0 over the last `window` and the first `sinks` ones only. scale:
+    1 / sqrt(D) by default. Returns out (q's type unless given), or (out, lse) with lse fp32 [rows][Hq]
+    when lse is given or want_lse. Rows of no sequence are left as they are; a row that sees nothing gets
+    0 and -inf."""
+    Hq = q.shape[1] if q.dim() == 3 else 0
+    dq = _rows_desc(q, "q", cache, batch, Hq)
+    if out is None:
+        out = torch.empty((q.shape[0], Hq, cache.D), dtype=q.dtype, device=q.device)
+    do = _rows_desc(out, "out", cache, batch, Hq)
+    if lse is None and want_lse:
+        lse = torch.empty((q.shape[0], Hq), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _dev(lse, "lse")
+        if lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape[0] < batch.rows or lse.shape[1] != Hq \
+                or lse.device != cache.device:
+            raise ValueError(f"lse must be float32 [{batch.rows} or more][{Hq}] on the cache's device")
+    if workspace is None:
+        workspace = kv_attention_workspace(cache, batch, Hq, window, sinks)
+    elif workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the cache's device")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _kv_call(cache, batch, lib().w4_kv_attention, cache._ref, batch._ref, dq, Hq,
+             cache.D ** -0.5 if scale is None else scale, window, sinks, do, _ptr(lse), _ptr(workspace), nbytes)
+    return out if lse is None else (out, lse)
 
 
 MOE_SCRATCH_BYTES = 16 << 20

@@ -1,5 +1,6 @@
 // C-ABI entry points: host-side validation, error reporting and dispatch.
 // Every check runs before anything is enqueued, so a failing call launches nothing.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -8,6 +9,7 @@
 #include <mutex>
 
 #include "../../include/w4a16.h"
+#include "kv_attention.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -757,6 +759,207 @@ int w4_kv_weighted_sum_append(const float* p, const float* v_new, int64_t n, int
         e = w4::launch_kv_weighted_sum(p, Hq, Hkv, T, T_max, v_codes, v_scales, out,
                                        (float*)workspace, nullptr, 0, st);
     return hip_status(e, "kv_weighted_sum_append launches");
+}
+
+// ---------------------------------------------------------------- batched INT4 KV cache
+static const int64_t kInt31 = 0x7fffffffLL;
+
+// Checks the pool and the batch and gives the kernels' view of them. B == 0 and
+// rows == 0 leave *v unset: the caller returns at once.
+static int kv_check_pages(const w4_kv_pages* c, const w4_kv_batch* b, w4::KvPages* v) {
+    if (!c || !b) return fail(W4_EINVAL, "null cache or batch");
+    if (c->D != 64 && c->D != 128 && c->D != 256)
+        return fail(W4_ESHAPE, "D=%d: head vectors of 64, 128 or 256 values", (int)c->D);
+    if (c->Hkv < 1 || c->num_pages < 1 || c->page_size < 1 || c->num_pages > kInt31 ||
+        c->page_size > kInt31 || c->Hkv > 65535)
+        return fail(W4_ESHAPE, "num_pages=%lld Hkv=%lld page_size=%lld out of range",
+                    (long long)c->num_pages, (long long)c->Hkv, (long long)c->page_size);
+    if (b->B < 0 || b->rows < 0 || b->max_rows < 0 || b->max_len < 0 || b->B > (1 << 20) ||
+        b->rows > kInt31 / c->Hkv)
+        return fail(W4_ESHAPE, "B=%lld rows=%lld max_rows=%lld max_len=%lld out of range",
+                    (long long)b->B, (long long)b->rows, (long long)b->max_rows, (long long)b->max_len);
+    if (b->B == 0 || b->rows == 0) return W4_OK;
+    if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales || !b->lens)
+        return fail(W4_EINVAL, "null codes, scales or lens");
+    if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) ||
+        !aligned16(c->v_scales))
+        return fail(W4_EALIGN, "codes and scales must be 16-byte aligned");
+    if (((uintptr_t)b->lens | (uintptr_t)b->starts | (uintptr_t)b->table) & 3u)
+        return fail(W4_EALIGN, "lens, starts and table must be 4-byte aligned");
+    if (!b->starts && b->rows % b->B)
+        return fail(W4_ESHAPE, "rows=%lld over B=%lld sequences without starts", (long long)b->rows,
+                    (long long)b->B);
+    int64_t cap = c->page_size;
+    int shift = 0;
+    if (b->table) {
+        if (c->page_size < 16 || (c->page_size & (c->page_size - 1)))
+            return fail(W4_ESHAPE, "page_size=%lld: a power of two, 16 or more, with a table",
+                        (long long)c->page_size);
+        if (b->table_width < 1 || b->table_stride < b->table_width ||
+            b->table_width > kInt31 / c->page_size)
+            return fail(W4_ESHAPE, "table_width=%lld table_stride=%lld out of range",
+                        (long long)b->table_width, (long long)b->table_stride);
+        cap *= b->table_width;
+        while ((1LL << shift) < c->page_size) ++shift;
+    } else if (c->num_pages < b->B) {
+        return fail(W4_ESHAPE, "%lld pages for %lld sequences without a table",
+                    (long long)c->num_pages, (long long)b->B);
+    }
+    v->codes[0] = c->k_codes;
+    v->codes[1] = c->v_codes;
+    v->scales[0] = c->k_scales;
+    v->scales[1] = c->v_scales;
+    v->Hkv = (int)c->Hkv;
+    v->page_size = (int)c->page_size;
+    v->page_shift = shift;
+    v->num_pages = (int)c->num_pages;
+    v->lens = b->lens;
+    v->starts = b->starts;
+    v->table = b->table;
+    v->table_stride = b->table_stride;
+    v->capacity = (int)cap;
+    v->B = (int)b->B;
+    v->rows = (int)b->rows;
+    v->even_rows = b->starts ? 0 : (int)(b->rows / b->B);
+    return W4_OK;
+}
+
+// The rows of one sequence that the launch is laid out for: the caller's bound,
+// or all of them where it gives none.
+static int64_t kv_max_rows(const w4_kv_batch* b) {
+    if (!b->starts) return b->rows / b->B;
+    return b->max_rows > 0 && b->max_rows < b->rows ? b->max_rows : b->rows;
+}
+static int64_t kv_max_len(const w4_kv_batch* b, const w4::KvPages& v) {
+    return b->max_len > 0 && b->max_len < v.capacity ? b->max_len : v.capacity;
+}
+
+static int kv_check_rows(const w4_rows* t, const char* name, int64_t rows, int64_t heads, int D,
+                         bool written) {
+    if (!t->data) return fail(W4_EINVAL, "%s: null data", name);
+    if (t->dtype != W4_F32 && t->dtype != W4_BF16)
+        return fail(W4_EINVAL, "%s: unknown type %d", name, (int)t->dtype);
+    if (!aligned16(t->data)) return fail(W4_EALIGN, "%s must be 16-byte aligned", name);
+    const int64_t unit = t->dtype == W4_BF16 ? 8 : 4;  // values in 16 bytes
+    const int64_t rs = rows > 1 ? t->row_stride : 0, hs = heads > 1 ? t->head_stride : 0;
+    if (rs < 0 || hs < 0 || rs > (1LL << 40) || hs > (1LL << 40))
+        return fail(W4_ESHAPE, "%s: strides %lld, %lld out of range", name, (long long)t->row_stride,
+                    (long long)t->head_stride);
+    if (rs % unit || hs % unit)
+        return fail(W4_EALIGN, "%s: strides %lld, %lld must be multiples of 16 bytes", name,
+                    (long long)t->row_stride, (long long)t->head_stride);
+    if (!written) return W4_OK;
+    const bool heads_inside = (heads == 1 || hs >= D) && (rows == 1 || rs >= (heads - 1) * hs + D);
+    const bool rows_inside = (rows == 1 || rs >= D) && (heads == 1 || hs >= (rows - 1) * rs + D);
+    if (!heads_inside && !rows_inside)
+        return fail(W4_ESHAPE, "%s: strides %lld, %lld make vectors overlap", name,
+                    (long long)t->row_stride, (long long)t->head_stride);
+    return W4_OK;
+}
+
+static int kv_rows_call(bool write, const w4_kv_pages* cache, const w4_kv_batch* batch,
+                        const w4_rows* k, const w4_rows* v, void* stream) {
+    w4::KvPages view;
+    int rc = kv_check_pages(cache, batch, &view);
+    if (rc) return rc;
+    if (batch->B == 0 || batch->rows == 0) return ok();
+    const w4_rows* t[2] = {k, v};
+    void* data[2] = {nullptr, nullptr};
+    int64_t rs[2] = {0, 0}, hs[2] = {0, 0};
+    for (int i = 0; i < 2; ++i) {
+        if (!t[i]) continue;
+        rc = kv_check_rows(t[i], i ? "v" : "k", batch->rows, cache->Hkv, cache->D, !write);
+        if (rc) return rc;
+        data[i] = t[i]->data;
+        rs[i] = t[i]->row_stride;
+        hs[i] = t[i]->head_stride;
+    }
+    if (!k && !v) return fail(W4_EINVAL, "both k and v are null");
+    // one launch serves both where they are of one type
+    const int64_t max_rows = kv_max_rows(batch);
+    for (int bf16 = 0; bf16 < 2; ++bf16) {
+        void* d[2];
+        for (int i = 0; i < 2; ++i) d[i] = t[i] && (t[i]->dtype == W4_BF16) == (bf16 == 1) ? data[i] : nullptr;
+        if (!d[0] && !d[1]) continue;
+        const hipError_t e = w4::launch_kv_rows(write, cache->D, bf16 == 1, view, d, rs, hs, (int)max_rows,
+                                                (hipStream_t)stream);
+        if (e != hipSuccess) return hip_status(e, write ? "kv_write launch" : "kv_read launch");
+    }
+    return ok();
+}
+
+int w4_kv_write(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows* k,
+                const w4_rows* v, void* stream) {
+    return kv_rows_call(true, cache, batch, k, v, stream);
+}
+
+int w4_kv_read(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows* k,
+               const w4_rows* v, void* stream) {
+    return kv_rows_call(false, cache, batch, k, v, stream);
+}
+
+// Query heads and mask; the sizes of the launch
+static int kv_check_heads(const w4_kv_pages* c, const w4_kv_batch* b, int64_t Hq, int64_t window,
+                          int64_t sinks) {
+    if (Hq < 1 || Hq % c->Hkv || Hq > kInt31 / (b->rows > 0 ? b->rows : 1))
+        return fail(W4_ESHAPE, "Hq=%lld must be a positive multiple of Hkv=%lld, with rows * Hq in 31 bits",
+                    (long long)Hq, (long long)c->Hkv);
+    if (window < 0 || sinks < 0)
+        return fail(W4_ESHAPE, "window=%lld sinks=%lld out of range", (long long)window, (long long)sinks);
+    return W4_OK;
+}
+
+size_t w4_kv_attention_workspace_bytes(const w4_kv_pages* cache, const w4_kv_batch* batch,
+                                       int64_t Hq, int64_t window, int64_t sinks) {
+    w4::KvPages v;
+    if (kv_check_pages(cache, batch, &v) || batch->B == 0 || batch->rows == 0 ||
+        kv_check_heads(cache, batch, Hq, window, sinks))
+        return 0;
+    return w4::kv_attention_workspace(v, cache->D, Hq, kv_max_rows(batch), kv_max_len(batch, v),
+                                      window, sinks);
+}
+
+int w4_kv_attention(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows* q,
+                    int64_t Hq, float scale, int64_t window, int64_t sinks, const w4_rows* out,
+                    float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    w4::KvPages v;
+    int rc = kv_check_pages(cache, batch, &v);
+    if (rc) return rc;
+    rc = kv_check_heads(cache, batch, Hq, window, sinks);
+    if (rc) return rc;
+    if (!isfinite(scale)) return fail(W4_EINVAL, "scale is not finite");
+    if (batch->B == 0 || batch->rows == 0) return ok();
+    if (!q || !out) return fail(W4_EINVAL, "null q or out");
+    rc = kv_check_rows(q, "q", batch->rows, Hq, cache->D, false);
+    if (rc) return rc;
+    rc = kv_check_rows(out, "out", batch->rows, Hq, cache->D, true);
+    if (rc) return rc;
+    if ((uintptr_t)lse & 15u) return fail(W4_EALIGN, "lse must be 16-byte aligned");
+    const int64_t max_rows = kv_max_rows(batch), max_len = kv_max_len(batch, v);
+    const size_t need = w4::kv_attention_workspace(v, cache->D, Hq, max_rows, max_len, window, sinks);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(W4_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                    workspace ? workspace_bytes : (size_t)0);
+    if (need && !aligned16(workspace)) return fail(W4_EALIGN, "workspace must be 16-byte aligned");
+    w4::KvAttn a;
+    a.q = q->data;
+    a.out = out->data;
+    a.lse = lse;
+    a.work = need ? workspace : nullptr;
+    a.q_row = q->row_stride;
+    a.q_head = q->head_stride;
+    a.out_row = out->row_stride;
+    a.out_head = out->head_stride;
+    a.Hq = (int)Hq;
+    a.group = (int)(Hq / cache->Hkv);
+    a.window = (int)(window < kInt31 ? window : kInt31);
+    a.sinks = (int)(sinks < kInt31 ? sinks : kInt31);
+    a.max_rows = (int)max_rows;
+    a.max_len = (int)max_len;
+    a.scale = scale;
+    return hip_status(w4::launch_kv_attention(cache->D, q->dtype == W4_BF16, out->dtype == W4_BF16, v, a,
+                                              (hipStream_t)stream),
+                      "kv_attention launch");
 }
 
 }  // extern "C"

@@ -450,6 +450,121 @@ int w4_kv_weighted_sum_append(const float* p, const float* v_new, int64_t n, int
                               float* v_scales, float* out, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/*
+ * Batched INT4 KV cache: many sequences in one pool of pages, and attention over
+ * it. The codec is the one above, per head vector of D values, so a cache made
+ * by w4_kv_quantize (codes [Hkv][T_max][64], scales [Hkv][T_max]) is a pool of
+ * one page of T_max positions with D = 128.
+ *
+ * w4_kv_pages: the pool. codes uint8 [num_pages][Hkv][page_size][D / 2], scales
+ * fp32 [num_pages][Hkv][page_size]; one head's positions of a page are
+ * contiguous. D is 64, 128 or 256. Codes are 16-byte aligned, scales too.
+ *
+ * w4_kv_batch: which rows and pages belong to which sequence. The three arrays
+ * are device memory that the kernels read when they run, so a captured graph
+ * replays with the contents of that moment; the other fields are host values.
+ *   lens [B]: positions sequence b holds, the rows of this call included; each
+ *     in [0, capacity], where capacity = table_width * page_size (with a table)
+ *     or page_size.
+ *   starts [B + 1], ascending, or NULL: rows starts[b] .. starts[b + 1] - 1 of
+ *     the packed row tensors are sequence b's last positions, row i of its n
+ *     at position lens[b] - n + i. NULL: every sequence has rows / B rows
+ *     (rows must be a multiple of B). Rows of no sequence are left as they are.
+ *   table [B][table_stride] or NULL: entry j of sequence b is the page that
+ *     holds its positions j * page_size and up (j < table_width <=
+ *     table_stride); page_size is then a power of two, 16 or more. NULL:
+ *     sequence b owns page b (num_pages >= B) and page_size is any size.
+ *   rows: rows of the packed tensors, at most. max_rows: the most rows of one
+ *     sequence, and max_len: the largest of lens; both only shape the launch
+ *     (speed, not results), 0 if unknown.
+ * Contents are not trusted with memory: a page outside [0, num_pages) holds no
+ * position (nothing is written to it, it reads back as zeros, attention does
+ * not see it), lens are clamped to [0, capacity] and starts to [0, rows], and a
+ * row whose position is negative is at no position (not written, reads back as
+ * zeros, sees nothing). One position must not belong to two rows of a call to
+ * w4_kv_write.
+ */
+typedef struct w4_kv_pages {
+    int32_t D;
+    int64_t num_pages, Hkv, page_size;
+    uint8_t* k_codes;
+    float* k_scales;
+    uint8_t* v_codes;
+    float* v_scales;
+} w4_kv_pages;
+
+typedef struct w4_kv_batch {
+    int64_t B, rows, max_rows, max_len;
+    const int32_t* lens;
+    const int32_t* starts;
+    const int32_t* table;
+    int64_t table_width, table_stride;
+} w4_kv_batch;
+
+/*
+ * A row tensor [rows][heads][D] of fp32 or bf16 values: element (r, h, i) at
+ * data + r * row_stride + h * head_stride + i, strides in elements, so that the
+ * slices of one Q-K-V matrix or a [heads][rows][D] tensor need no copy. data is
+ * 16-byte aligned and the strides are multiples of 16 bytes (strides of
+ * dimensions of size 1 do not matter). Vectors of a tensor that is written must
+ * not overlap.
+ */
+#define W4_F32  0
+#define W4_BF16 1
+typedef struct w4_rows {
+    void* data;
+    int32_t dtype; /* W4_F32 or W4_BF16 */
+    int64_t row_stride, head_stride;
+} w4_rows;
+
+/*
+ * Quantize the batch's rows of keys and values into the cache, in one launch:
+ * k, v [rows][Hkv][D], either may be NULL (that half is not written). Codes and
+ * scales equal w4_kv_quantize's on the same values (a bf16 value counts as the
+ * fp32 value it is), bit for bit.
+ */
+int w4_kv_write(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows* k,
+                const w4_rows* v, void* stream);
+
+/*
+ * The inverse: the batch's rows read back, (nibble - 8) * scale in fp32, rounded
+ * to the row tensor's type (to nearest even). Either of k, v may be NULL. All
+ * positions of a sequence are read by giving it as many rows as it holds
+ * positions.
+ */
+int w4_kv_read(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows* k,
+               const w4_rows* v, void* stream);
+
+/*
+ * Attention over the cache with the dequantization fused in ([Shimmy] §3.2: the
+ * shader dequantizes while it computes attention), for single tokens and for
+ * prompts. The row at position p of sequence b, query head h, sees the cached
+ * positions
+ *   t with 0 <= t <= p and (window == 0 or t > p - window or t < sinks)
+ * of kv head h / (Hq / Hkv): causal, with window > 0 only the last `window`
+ * positions and the first `sinks` ones. With z_t = scale * sum_i q[i] k[t][i]
+ * over those,
+ *   out = sum_t exp(z_t) v[t] / sum_t exp(z_t),   lse = log sum_t exp(z_t);
+ * a row that sees nothing gets out = 0 and lse = -infinity. The rows' own keys
+ * and values are read from the cache: write them first.
+ * q [rows][Hq][D] and out [rows][Hq][D], each fp32 or bf16 on its own; Hq a
+ * multiple of Hkv; lse fp32 [rows][Hq] contiguous, or NULL; window, sinks >= 0
+ * (sinks without a window change nothing); scale finite. workspace: device
+ * memory of at least w4_kv_attention_workspace_bytes(...) bytes for the same
+ * cache, batch (its host values), Hq, window and sinks (W4_EWORKSPACE
+ * otherwise; may be NULL when that is 0); its contents on entry do not matter,
+ * on return they are unspecified. Calls sharing a workspace must not overlap.
+ * Softmax statistics and sums are fp32; the products run on the matrix cores
+ * with the codes as exact 16-bit integers, a bf16 query exact and an fp32 one
+ * in two pieces of 11 bits. Deterministic for given arguments; max_rows and
+ * max_len may change the order of sums.
+ */
+size_t w4_kv_attention_workspace_bytes(const w4_kv_pages* cache, const w4_kv_batch* batch,
+                                       int64_t Hq, int64_t window, int64_t sinks);
+int w4_kv_attention(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows* q,
+                    int64_t Hq, float scale, int64_t window, int64_t sinks, const w4_rows* out,
+                    float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Message for the last non-zero return on the calling thread ("" if none). */
 const char* w4_last_error(void);
 

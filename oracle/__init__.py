@@ -22,12 +22,12 @@ from .quant import (SCHEMES, GROUP, BITS, bf16_round, bf16_to_f32, quantize, qua
                     quantize_affine, pack, unpack, dequantize, quantize_pack, packed_nbytes)
 from .matmul import matmul_f64, abs_matmul_f64, gemv_reference
 from .moe import route, gelu_tanh, ffn, moe_sparse, moe_dense_masked
-from .kv import kv_quantize, kv_unpack, kv_dequant, kv_scores, kv_weighted_sum
+from .kv import kv_quantize, kv_unpack, kv_dequant, kv_scores, kv_weighted_sum, kv_attention
 
 __all__ = [
     "SCHEMES", "GROUP", "BITS", "bf16_round", "bf16_to_f32", "quantize", "quantize_sym4",
     "quantize_affine", "pack", "unpack", "dequantize", "quantize_pack", "packed_nbytes",
     "matmul_f64", "abs_matmul_f64", "gemv_reference", "route", "gelu_tanh", "ffn",
     "moe_sparse", "moe_dense_masked", "kv_quantize", "kv_unpack", "kv_dequant", "kv_scores",
-    "kv_weighted_sum",
+    "kv_weighted_sum", "kv_attention",
 ]

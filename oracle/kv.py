@@ -100,3 +100,38 @@ def kv_weighted_sum(p: np.ndarray, codes: np.ndarray, scale: np.ndarray):
     y = np.stack([p64[h] @ Vd[g[h]] for h in range(p64.shape[0])])
     S = np.stack([np.abs(p64[h]) @ np.abs(Vd[g[h]]) for h in range(p64.shape[0])])
     return y, S
+
+
+def kv_attention(q, k, v, scale, window=0, sinks=0):
+    """Causal attention of one sequence's last n positions over its dequantized cache, in fp64.
+
+    q [n][Hq][D]; k, v [Hkv][L][D]; row i stands at position L - n + i and sees t <= its position,
+    with window > 0 only t > position - window or t < sinks. Hidden keys' values do not enter, whatever
+    they are. Returns out [n][Hq][D], lse [n][Hq], and what tolerances are made of: A [n][Hq][D] =
+    sum_t p_t |v_t|, Z [n][Hq] = max over visible t of scale * sum_i |q_i||k_ti|, and Zmax [n][Hq] = the
+    same with max|q| for every |q_i|. A row that sees nothing: out 0, lse -inf, the rest 0."""
+    q = np.asarray(q, dtype=np.float64)
+    n, Hq, D = q.shape
+    L = k.shape[1]
+    g = _group_of(Hq, k.shape[0])
+    out, A = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
+    lse = np.full((n, Hq), -np.inf)
+    Z, Zmax = np.zeros((n, Hq)), np.zeros((n, Hq))
+    for i in range(n):
+        p = L - n + i
+        t = np.arange(max(p + 1, 0))
+        if window > 0:
+            t = t[(t > p - window) | (t < sinks)]
+        if t.size == 0:
+            continue
+        for h in range(Hq):
+            K, V, x = k[g[h]][t], v[g[h]][t], q[i, h]
+            z = scale * (K @ x)
+            m = z.max()
+            e = np.exp(z - m)
+            out[i, h] = e @ V / e.sum()
+            A[i, h] = e @ np.abs(V) / e.sum()
+            lse[i, h] = m + np.log(e.sum())
+            Z[i, h] = (abs(scale) * (np.abs(K) @ np.abs(x))).max()
+            Zmax[i, h] = (abs(scale) * np.abs(K).sum(1) * np.abs(x).max()).max()
+    return out, lse, A, Z, Zmax

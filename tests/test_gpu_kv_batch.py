@@ -1,0 +1,426 @@
+"""GPU parity of the batched INT4 KV cache: rows written and read back bit for bit
+against the oracle's codec, attention for single tokens and prompts within bounds
+derived from the arithmetic (kv_batch_util.bounds), and the cases where such kernels go
+wrong: empty rows, stale memory, bad pages, strides, padding, replayed graphs, streams."""
+import numpy as np
+import pytest
+import torch
+
+import bit_weight_only_quantize_amd as w4
+import oracle
+from kv_batch_util import DT, Batch, bounds, to_dev, values
+
+pytestmark = pytest.mark.gpu
+
+
+def _bits(t):
+    return t.contiguous().view(torch.uint8).cpu().numpy()
+
+
+# ---------------------------------------------------------------- write and read
+@pytest.mark.parametrize("lens,rows,Hkv,D,page,dtype", [
+    ([1], [1], 1, 128, 0, "f32"),
+    ([5, 300, 17], [1, 1, 1], 32, 128, 64, "f32"),            # one token for each of three sequences
+    ([37, 0, 250, 3], [37, 0, 201, 1], 3, 64, 16, "bf16"),    # ragged prompts, an empty sequence
+    ([100, 129], [33, 129], 5, 256, 32, "f32"),
+    ([77, 64], [70, 64], 8, 128, 0, "bf16"),                  # no table
+    ([2], [5], 2, 128, 16, "f32"),                            # more rows than positions: three at none
+])
+def test_write_and_read(lens, rows, Hkv, D, page, dtype):
+    s = Batch(lens, rows, Hkv, D, page, f"wr.{lens}.{D}", vec_dtype=dtype)
+    old = [L - min(L, n) for L, n in zip(lens, rows)]
+    cache = s.cache(upto=old)
+    b = s.batch(max_rows=max(rows))
+    k, v = (to_dev(s.new_rows(i), dtype) for i in (0, 1))
+    w4.kv_write(k, v, cache, b)
+    for got, want in zip((cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales), s.host_pool()):
+        assert np.array_equal(_bits(got), want.view(np.uint8).reshape(_bits(got).shape)), "cache differs"
+    # read back everything the sequences hold, and the call's rows, in both types
+    full = Batch(lens, lens, Hkv, D, page, f"wr.{lens}.{D}", vec_dtype=dtype)
+    for src, batch in ((full, full.batch()), (s, b)):
+        for out in ("f32", "bf16"):
+            got = w4.kv_read(cache, batch, dtype=DT[out])
+            for i in (0, 1):
+                want = np.zeros((src.rows, Hkv, D))
+                for q in range(src.B):
+                    m = min(src.lens[q], src.n[q])
+                    at = src.first[q] + src.n[q]
+                    want[at - m:at] = s.deq[i][q][:, src.lens[q] - m:].transpose(1, 0, 2)
+                w32 = torch.from_numpy(want.astype(np.float32)).to(DT[out])
+                assert torch.equal(got[i].cpu(), w32), f"{out} rows differ"
+
+
+def test_write_equals_the_single_sequence_codec():
+    """A pool of one page is w4_kv_quantize's cache: the same bytes, and its products read it."""
+    Hkv, L = 4, 70
+    x = values((L, Hkv, 128), "one.k")
+    x[3] = 0.0
+    x[4, 1, :11] = [7.5, 0.5, -0.5, 1.5, -1.5, 2.5, -2.5, 3.5, -3.5, 6.5, -6.5]
+    x[4, 1, 11:] = 0.0
+    x[5] = np.float32(1e-44)                                   # least subnormals: the scale itself rounds
+    x[6] = np.float32(3e38)
+    codes, scales = w4.kv_cache(Hkv, L)
+    xd = torch.from_numpy(x).cuda()
+    w4.kv_quantize(xd, codes, scales, 0)
+    cache = w4.kv_pages(1, Hkv, L)
+    batch = w4.KVBatch(torch.tensor([L], dtype=torch.int32, device="cuda"), rows=L)
+    w4.kv_write(xd, xd, cache, batch)
+    for c, s in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)):
+        assert torch.equal(c[0], codes) and torch.equal(s[0].view(torch.int32), scales.view(torch.int32))
+
+
+def test_write_one_half_and_mixed_types():
+    s = Batch([40, 9], [7, 2], 2, 64, 16, "half")
+    cache = s.cache(upto=[33, 7])
+    before = [t.clone() for t in (cache.v_codes, cache.v_scales)]
+    k = to_dev(s.new_rows(0), "f32")
+    w4.kv_write(k, None, cache, s.batch())
+    assert torch.equal(cache.v_codes, before[0])
+    assert torch.equal(cache.v_scales.view(torch.int32), before[1].view(torch.int32))
+    v16 = to_dev(s.new_rows(1), "f32").bfloat16()
+    w4.kv_write(k, v16, cache, s.batch())                      # fp32 keys, bf16 values
+    vr = torch.empty((9, 2, 64), dtype=torch.float32, device="cuda")
+    kr = torch.empty((9, 2, 64), dtype=torch.bfloat16, device="cuda")
+    w4.kv_read(cache, s.batch(), k=kr, v=vr)
+    c, sc = oracle.kv_quantize(v16.float().cpu().numpy())
+    assert np.array_equal(vr.cpu().numpy(), oracle.kv_dequant(c, sc).astype(np.float32))
+    only = torch.empty_like(vr)
+    assert w4.kv_read(cache, s.batch(), v=only)[0] is None and torch.equal(only, vr)
+
+
+def test_strided_rows_and_rows_behind_the_last_sequence():
+    Hkv, D = 3, 128
+    s = Batch([50, 21], [13, 4], Hkv, D, 16, "stride", vec_dtype="bf16")
+    rows = s.rows
+    fused = torch.zeros((rows + 5, (2 * Hkv + 4) * D), dtype=torch.bfloat16, device="cuda")
+    fused[:rows, 4 * D:(4 + Hkv) * D] = to_dev(s.new_rows(0), "bf16").view(rows, -1)
+    fused[:rows, (4 + Hkv) * D:] = to_dev(s.new_rows(1), "bf16").view(rows, -1)
+    k = fused[:, 4 * D:(4 + Hkv) * D].view(rows + 5, Hkv, D)
+    v = fused[:, (4 + Hkv) * D:].view(rows + 5, Hkv, D)
+    cache = s.cache(upto=[37, 17])
+    b = s.batch()
+    w4.kv_write(k, v, cache, b)
+    for got, want in zip((cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales), s.host_pool()):
+        assert np.array_equal(_bits(got), want.view(np.uint8).reshape(_bits(got).shape))
+    # read into [heads][rows][D] storage, with rows behind the last sequence
+    hold = torch.full((Hkv, rows + 5, D), 7.0, dtype=torch.float32, device="cuda")
+    kr = hold.transpose(0, 1)
+    w4.kv_read(cache, b, k=kr)
+    c, sc = oracle.kv_quantize(s.new_rows(0))
+    assert np.array_equal(kr[:rows].cpu().numpy(), oracle.kv_dequant(c, sc).astype(np.float32))
+    assert (kr[rows:] == 7.0).all()
+
+
+# ---------------------------------------------------------------- attention
+def _attend(s, Hq, q_dtype, out_dtype, scale=None, window=0, sinks=0, name="", **kw):
+    """One call over the batch against the oracle's; returns (out, lse)."""
+    q = values((s.rows, Hq, s.D), f"att.q.{name}", q_dtype, seed=2)
+    cache, b = s.cache(), s.batch(max_rows=max(s.n), max_len=max(s.lens), **kw)
+    out = torch.full((s.rows, Hq, s.D), 9.0, dtype=DT[out_dtype], device="cuda")
+    n = w4.lib().w4_kv_attention_workspace_bytes(cache._ref, b._ref, Hq, window, sinks)
+    ws = torch.full((max(n, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+    got, lse = w4.kv_attention(to_dev(q, q_dtype), cache, b, scale=scale, window=window, sinks=sinks, out=out,
+                               want_lse=True, workspace=ws)
+    torch.cuda.synchronize()
+    sc = float(np.float32(s.D ** -0.5 if scale is None else scale))
+    check(s, got, lse, s.attend(q, sc, window, sinks), q_dtype, out_dtype)
+    return got, lse
+
+
+def check(s, got, lse, ref, q_dtype, out_dtype):
+    vmax = max([np.abs(d).max() for d in s.deq[1] if d.size], default=0.0)
+    e, el = bounds(ref, s.D, max(max(s.lens), 1), vmax, q_dtype, out_dtype)
+    g, l = got.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    empty = ~np.isfinite(ref[1])
+    assert np.array_equal(np.isneginf(l), empty), "rows that see nothing"
+    assert np.all(g[empty] == 0)
+    assert np.isfinite(g).all()
+    worst = (np.abs(g - ref[0])[~empty] / e[~empty]).max() if (~empty).any() else 0.0
+    lw = (np.abs(l - np.where(empty, 0, ref[1]))[~empty] / el[~empty]).max() if (~empty).any() else 0.0
+    print(f"[kv_attention] out {worst:.3f} lse {lw:.3f} of the bounds", flush=True)
+    assert worst <= 1.0 and lw <= 1.0
+
+
+@pytest.mark.parametrize("q_dtype,out_dtype", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_types_and_head_sizes(D, q_dtype, out_dtype):
+    s = Batch([70, 333, 1], [1, 1, 1], 2, D, 16, f"types.{D}")
+    _attend(s, 6, q_dtype, out_dtype, name=f"d{D}")
+    s = Batch([70, 45], [70, 11], 2, D, 0, f"types.p{D}")
+    _attend(s, 6, q_dtype, out_dtype, name=f"p{D}")
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (4, 4), (5, 1), (16, 2), (17, 1), (40, 8), (71, 1)])
+def test_attention_head_groups(Hq, Hkv):
+    s = Batch([257, 31], [1, 1], Hkv, 128, 64, f"heads.{Hq}")
+    _attend(s, Hq, "bf16", "bf16", name=f"h{Hq}")
+    s = Batch([90], [9], Hkv, 128, 64, f"headsp.{Hq}")
+    _attend(s, Hq, "bf16", "f32", name=f"hp{Hq}")
+
+
+@pytest.mark.parametrize("L", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 500, 1023, 1025, 4099])
+def test_attention_one_token_lengths(L):
+    s = Batch([L, 0, max(1, L // 3)], [1, 1, 1], 2, 128, 0 if L % 2 else 16, f"len.{L}")
+    _attend(s, 8, "f32", "f32", name=f"l{L}")
+
+
+@pytest.mark.parametrize("lens,rows,page", [
+    ([1], [1], 0), ([2], [2], 16), ([64], [64], 0), ([65], [65], 16), ([200], [200], 32),
+    ([300, 40, 0, 129], [17, 40, 2, 1], 16),                   # a slot with rows and no position
+    ([5], [9], 16),                                            # four rows before the first position
+    ([700], [130], 64), ([257, 256, 255], [100, 1, 255], 128),
+])
+def test_attention_prompts(lens, rows, page):
+    s = Batch(lens, rows, 2, 128, page, f"prompt.{lens}")
+    _attend(s, 6, "bf16", "bf16", name="prompt")
+    _attend(s, 2, "f32", "f32", name="prompt1")
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (7, 3), (16, 16), (33, 4), (64, 70), (100, 5), (1000, 4),
+                                          (50, 10 ** 9), (2 ** 40, 2 ** 40)])
+@pytest.mark.parametrize("lens,rows", [([300, 20, 77], [1, 1, 1]), ([300, 45], [120, 45])])
+def test_attention_window_and_sinks(lens, rows, window, sinks):
+    s = Batch(lens, rows, 2, 64, 16, f"win.{lens}.{rows}")
+    _attend(s, 8, "f32", "f32", window=window, sinks=sinks, name="win")
+
+
+def test_attention_window_over_a_long_cache():
+    s = Batch([9000, 5000], [1, 3], 1, 64, 16, "winlong")
+    _attend(s, 4, "bf16", "f32", window=130, sinks=4, name="winlong")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1.0, 4.0])
+def test_attention_scales(scale):
+    s = Batch([150], [3], 2, 128, 16, "scale")
+    _attend(s, 4, "f32", "f32", scale=scale, name="scale")
+
+
+def test_attention_queries_of_extreme_magnitude():
+    """Zero rows, rows near the types' ends, elements far below their row's largest."""
+    s = Batch([100], [6], 1, 64, 16, "qmag")
+    q = values((6, 2, 64), "qmag.q")
+    q[0] = 0
+    q[1] *= np.float32(1e-30)
+    q[2] *= np.float32(1e-42)                                  # subnormals
+    q[3, :, 1:] *= np.float32(2.0 ** -26)
+    q[4] *= np.float32(30.0)
+    q[5] *= np.float32(1e-3)
+    got, lse = w4.kv_attention(torch.from_numpy(q).cuda(), s.cache(), s.batch(), want_lse=True)
+    check(s, got, lse, s.attend(q, float(np.float32(64 ** -0.5))), "f32", "f32")
+    # a row of huge values picks the largest score alone
+    big = values((6, 2, 64), "qmag.q") * np.float32(1e30)
+    got = w4.kv_attention(torch.from_numpy(big).cuda(), s.cache(), s.batch())
+    ref = s.attend(big, float(np.float32(64 ** -0.5)))[0]
+    assert np.abs(got.cpu().numpy() - ref).max() <= 2.0 ** -20 * np.abs(ref).max()
+
+
+def test_attention_values_of_very_different_scales():
+    """Small values under large weights, large ones later, zero vectors, and the reverse."""
+    for order in (1, -1):
+        s = Batch([400], [1], 1, 128, 16, f"vmag.{order}")
+        mag = np.exp2(np.linspace(-12, 6, 400))[::order].astype(np.float32)
+        mag[::7] = 0
+        v = s.x[1][0] * mag[None, :, None]
+        s.quant[1] = [oracle.kv_quantize(v)]
+        s.deq[1] = [oracle.kv_dequant(*s.quant[1][0])]
+        _attend(s, 4, "f32", "f32", name="vmag")
+        _attend(s, 4, "bf16", "bf16", name="vmag")
+
+
+def test_attention_growing_scores():
+    """Keys whose scores grow along the sequence: the running maximum moves at every step."""
+    s = Batch([600], [2], 1, 64, 16, "grow")
+    q = values((2, 3, 64), "grow.q")
+    k = q[0, 0] * np.linspace(0.01, 3.0, 600, dtype=np.float32)[:, None] + 0.1 * s.x[0][0][0]
+    for a in (k, k[::-1].copy()):
+        s.quant[0] = [oracle.kv_quantize(a[None].astype(np.float32))]
+        s.deq[0] = [oracle.kv_dequant(*s.quant[0][0])]
+        got, lse = w4.kv_attention(torch.from_numpy(q).cuda(), s.cache(), s.batch(), scale=1.0, want_lse=True)
+        check(s, got, lse, s.attend(q, 1.0), "f32", "f32")
+
+
+def test_attention_bad_pages_hold_no_position():
+    """Pages outside the pool are skipped: the result is that of the positions that are left."""
+    s = Batch([100, 60], [1, 20], 2, 128, 16, "bad")
+    q = values((s.rows, 4, 128), "bad.q")
+    cache, b = s.cache(), s.batch()
+    table = s.table.copy()
+    table[0, 2], table[1, 1] = s.pages, -1
+    table[0, 0] = 2 ** 31 - 1
+    b.table.copy_(torch.from_numpy(table))
+    got, lse = w4.kv_attention(torch.from_numpy(q).cuda(), cache, b, want_lse=True)
+    r = []
+    for seq in range(2):
+        for i in range(s.n[seq]):
+            p = s.lens[seq] - s.n[seq] + i
+            t = np.array([t for t in range(p + 1) if 0 <= table[seq, t // 16] < s.pages])
+            row = q[s.first[seq] + i][None]
+            r.append(oracle.kv_attention(row, s.deq[0][seq][:, t], s.deq[1][seq][:, t], float(np.float32(128 ** -0.5))))
+    check(s, got, lse, [np.concatenate(x) for x in zip(*r)], "f32", "f32")
+    full = Batch(s.lens, s.lens, 2, 128, 16, "bad").batch()
+    full.table.copy_(b.table)
+    k = w4.kv_read(cache, full, dtype=torch.float32)[0].cpu().numpy()
+    assert np.all(k[32:48] == 0) and np.all(k[:16] == 0) and np.all(k[116:132] == 0)
+    assert np.array_equal(k[16:32], s.deq[0][0][:, 16:32].transpose(1, 0, 2).astype(np.float32))
+    before = cache.k_codes.clone()
+    w4.kv_write(torch.zeros((160, 2, 128), device="cuda"), None, cache, full)
+    touched = np.ones(s.pages, bool)
+    touched[[p for seq in range(2) for j, p in enumerate(table[seq][:-(-s.lens[seq] // 16)]) if 0 <= p < s.pages]] = False
+    assert torch.equal(cache.k_codes[torch.from_numpy(touched).cuda()], before[torch.from_numpy(touched).cuda()])
+
+
+def test_attention_lens_and_starts_out_of_range_stay_in_memory():
+    """Contents that break the contract are bounded: no fault, and the sound sequences are right."""
+    s = Batch([100, 60, 40], [1, 1, 1], 2, 64, 16, "range")
+    q = values((3, 4, 64), "range.q")
+    ref = s.attend(q, 64 ** -0.5)[0]
+    cache, b = s.cache(), s.batch()
+    b.lens.copy_(torch.tensor([100, 2 ** 31 - 1, -5], dtype=torch.int32))
+    b.starts.copy_(torch.tensor([0, 1, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32))
+    out = w4.kv_attention(torch.from_numpy(q).cuda(), cache, b)
+    w4.kv_read(cache, b)
+    torch.cuda.synchronize()
+    assert np.abs(out[0].cpu().numpy() - ref[0]).max() < 1e-4
+
+
+def test_attention_strides_padding_and_hints():
+    """Q as a slice of a fused matrix, out [heads][rows][D], padded rows, and launch hints that are too
+    small, too large or missing: the same rows."""
+    Hq, Hkv, D = 6, 2, 128
+    s = Batch([150, 40, 33], [20, 1, 33], Hkv, D, 16, "pad")
+    q = values((s.rows, Hq, D), "pad.q", "bf16")
+    ref = s.attend(q, float(np.float32(D ** -0.5)))
+    fused = torch.full((s.rows + 7, (Hq + 2 * Hkv) * D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    fused[:s.rows, :Hq * D] = to_dev(q, "bf16").view(s.rows, -1)
+    qd = fused[:, :Hq * D].view(s.rows + 7, Hq, D)
+    cache = s.cache()
+    for kw in ({}, dict(max_rows=33, max_len=150), dict(max_rows=1, max_len=1), dict(max_rows=10 ** 6, max_len=10 ** 6),
+               dict(rows=s.rows + 7)):
+        hold = torch.full((Hq, s.rows + 7, D), 5.0, dtype=torch.float32, device="cuda")
+        lse = torch.full((s.rows + 7, Hq), 5.0, dtype=torch.float32, device="cuda")
+        got, _ = w4.kv_attention(qd, cache, s.batch(**kw), out=hold.transpose(0, 1), lse=lse)
+        check(s, got[:s.rows], lse[:s.rows], ref, "bf16", "f32")
+        assert (hold[:, s.rows:] == 5.0).all() and (lse[s.rows:] == 5.0).all(), "rows of no sequence written"
+
+
+def test_attention_equals_the_products_of_the_single_sequence_cache():
+    """Scores, softmax and weighted sum over the one-sequence cache give the same attention."""
+    Hq, Hkv, T = 8, 4, 200
+    k, v = w4.kv_cache(Hkv, T + 5), w4.kv_cache(Hkv, T + 5)
+    w4.kv_append(torch.from_numpy(values((T, Hkv, 128), "prod.k")).cuda(),
+                 torch.from_numpy(values((T, Hkv, 128), "prod.v")).cuda(), k, v, 0)
+    q = torch.from_numpy(values((Hq, 128), "prod.q")).cuda()
+    z = w4.kv_scores(q, *k, T) / np.float32(np.sqrt(128))
+    want = w4.kv_weighted_sum(torch.softmax(z, 1).contiguous(), *v)
+    cache = w4.KVPages(k[0][None], k[1][None], v[0][None], v[1][None])
+    got = w4.kv_attention(q[None], cache, w4.KVBatch(torch.tensor([T], dtype=torch.int32, device="cuda")))
+    assert (got[0] - want).abs().max() <= 2.0 ** -16 * want.abs().max()
+
+
+# ---------------------------------------------------------------- as they are used together
+def test_prompt_then_tokens_in_a_replayed_graph():
+    """A ragged prompt is written and attended, then single tokens through one captured graph whose
+    lengths advance on the device; every replay against the eager call and the oracle."""
+    Hq, Hkv, D, steps = 8, 2, 128, 5
+    total = [77, 130, 20]
+    s = Batch(total, total, Hkv, D, 16, "run", vec_dtype="bf16")
+    q = values((s.rows, Hq, D), "run.q", "bf16")
+    ref = s.attend(q, float(np.float32(D ** -0.5)))
+    cache = s.cache(upto=[0, 0, 0])
+    pick = lambda b, lo, hi: np.arange(s.first[b] + lo, s.first[b] + hi)
+    head = np.concatenate([pick(b, 0, L - steps) for b, L in enumerate(total)])
+    kn, vn = s.new_rows(0), s.new_rows(1)
+    lens = torch.tensor([L - steps for L in total], dtype=torch.int32, device="cuda")
+    starts = torch.tensor(np.concatenate([[0], np.cumsum([L - steps for L in total])]), dtype=torch.int32, device="cuda")
+    table = torch.from_numpy(s.table).cuda()
+    prompt = w4.KVBatch(lens.clone(), table=table, starts=starts, rows=len(head))
+    w4.kv_write(to_dev(kn[head], "bf16"), to_dev(vn[head], "bf16"), cache, prompt)
+    got, lse = w4.kv_attention(to_dev(q[head], "bf16"), cache, prompt, want_lse=True)
+    check(s, got, lse, [r[head] for r in ref], "bf16", "bf16")
+    # tokens
+    tok = w4.KVBatch(lens, table=table, max_len=max(total))
+    kb, vb = (torch.empty((3, Hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qb, ob = (torch.empty((3, Hq, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lb = torch.empty((3, Hq), dtype=torch.float32, device="cuda")
+    ws = w4.kv_attention_workspace(cache, tok, Hq)
+
+    def step():
+        lens.add_(1)
+        w4.kv_write(kb, vb, cache, tok)
+        w4.kv_attention(qb, cache, tok, out=ob, lse=lb, workspace=ws)
+
+    saved = lens.clone()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        kb.zero_(), vb.zero_(), qb.zero_()
+        step()                                                  # warm up; its row is overwritten below
+    torch.cuda.synchronize()
+    lens.copy_(saved)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for j in range(steps):
+        now = np.array([s.first[b] + L - steps + j for b, L in enumerate(total)])
+        kb.copy_(to_dev(kn[now], "bf16")), vb.copy_(to_dev(vn[now], "bf16")), qb.copy_(to_dev(q[now], "bf16"))
+        g.replay()
+        torch.cuda.synchronize()
+        check(s, ob, lb, [r[now] for r in ref], "bf16", "bf16")
+        eager = w4.kv_attention(qb, cache, tok, workspace=ws)
+        assert torch.equal(eager, ob)
+    back = w4.kv_read(cache, w4.KVBatch(lens, table=table, starts=torch.from_numpy(s.first).cuda(), rows=s.rows),
+                      dtype=torch.float32)
+    for i in (0, 1):
+        want = np.concatenate([d.transpose(1, 0, 2) for d in s.deq[i]]).astype(np.float32)
+        assert np.array_equal(back[i].cpu().numpy(), want)
+
+
+def test_two_streams_and_repeated_calls_give_the_same_bits():
+    s = Batch([3000, 700], [1, 1], 4, 128, 64, "streams")
+    q = to_dev(values((2, 16, 128), "streams.q"), "f32")
+    cache, b = s.cache(), s.batch(starts=False, max_len=3000)
+    first = w4.kv_attention(q, cache, b)
+    torch.cuda.synchronize()
+    a, c = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(4):
+        for st in (a, c):
+            with torch.cuda.stream(st):
+                outs.append(w4.kv_attention(q, cache, b))
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, o) for o in outs)
+
+
+def test_sequences_that_share_pages():
+    """Two sequences over one prefix: the shared pages are read by both, as lens and table say."""
+    s = Batch([64, 80], [1, 1], 2, 128, 16, "share")
+    table = s.table.copy()
+    table[1, :4] = table[0, :4]
+    cache, b = s.cache(), s.batch()
+    b.table.copy_(torch.from_numpy(table))
+    q = values((2, 4, 128), "share.q")
+    got, lse = w4.kv_attention(torch.from_numpy(q).cuda(), cache, b, want_lse=True)
+    for half in s.deq:
+        half[1] = half[1].copy()
+        half[1][:, :64] = half[0]
+    check(s, got, lse, s.attend(q, float(np.float32(128 ** -0.5))), "f32", "f32")
+
+
+def test_positions_past_2_to_31_bytes():
+    """A cache whose offsets pass 32 bits: the far end of a 36-million-position page."""
+    L = 36_000_000                                              # 64-byte codes: 2.3e9 bytes a half
+    cache = w4.kv_pages(1, 1, L, 128)
+    for t in (cache.k_scales, cache.v_scales):
+        t.fill_(float("nan"))
+    x = values((40, 1, 128), "far.x")
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    b = w4.KVBatch(lens, rows=40)
+    xd = torch.from_numpy(x).cuda()
+    w4.kv_write(xd, xd, cache, b)
+    c, sc = oracle.kv_quantize(x[:, 0])
+    deq = oracle.kv_dequant(c, sc)
+    assert np.array_equal(w4.kv_read(cache, b, dtype=torch.float32)[0][:, 0].cpu().numpy(), deq.astype(np.float32))
+    q = values((1, 3, 128), "far.q")
+    got, lse = w4.kv_attention(torch.from_numpy(q).cuda(), cache, w4.KVBatch(lens), window=40, want_lse=True)
+    ref = oracle.kv_attention(q, deq[None], deq[None], float(np.float32(128 ** -0.5)))
+    e, el = bounds(ref, 128, 40, np.abs(deq).max(), "f32", "f32")
+    assert (np.abs(got.cpu().numpy() - ref[0]) <= e).all() and (np.abs(lse.cpu().numpy() - ref[1]) <= el).all()
