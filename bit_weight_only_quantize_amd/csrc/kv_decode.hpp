@@ -1,0 +1,368 @@
+// Attention over the batched INT4 KV cache with the keys split: the kernel for
+// few rows a sequence (single tokens above all).
+//
+//   z_t = scale * s_k[t] * sum_i q[i] c_k[t][i]   over the visible t
+//   out = sum_t exp(z_t) s_v[t] c_v[t] / sum_t exp(z_t)
+// in one pass over the keys, with the softmax's maximum and sum kept running.
+//
+// A workgroup takes one (sequence, kv head), up to 16 NC of its (row, query
+// head) columns and one part of its tiles of 32 keys; its four wavefronts take
+// the tiles in turn, straight from memory to registers (kv_tile.hpp), and meet
+// through LDS at the end. Parts of a sequence meet in kv_join_kernel.
+#pragma once
+
+#include <type_traits>
+
+#include "kv_tile.hpp"
+
+namespace w4 {
+
+// How one call is laid out; host values only, so that the workspace's size is
+// known before the call.
+struct KvPlan {
+    int column_tiles;  // of the sequence with the most rows
+    int nc;            // 16-column tiles a workgroup takes at once
+    int splits;        // parts of a sequence's keys
+};
+KvPlan kv_plan(const KvPages& c, int D, int group, int64_t max_rows, int64_t max_len, int64_t window,
+               int64_t sinks);
+
+// Partial results of a part: out[D] unnormalized, then the exponent's reference
+// (base 2) and the sum.
+__host__ __device__ inline int kv_partial_floats(int D) { return D + 4; }
+inline size_t kv_partial_bytes(int64_t vectors, int splits, int D) {
+    return (size_t)vectors * splits * kv_partial_floats(D) * sizeof(float);
+}
+
+// The running softmax of one column on its four lanes. With x the score times
+// the key's scale (one fma with the reference mx) weights are 2^((x - mx) c):
+// exactly 1 at the reference, however large x c is. mx follows the maximum
+// lazily, once a weight would pass 2^kLift, so that most tiles scale nothing.
+constexpr float kLift = 4.f;
+// Weights times value scales enter the second product as 16-bit floats. Value
+// scales are taken relative to 2^e, e the exponent of the largest so far,
+// which is raised once a scale reaches 8 * 2^e; with 2^kBoost on top the operand
+// stays below 2^(kLift + 3 + kBoost) = 2^15, and what the format's least step
+// drops is 2^-33 of the largest value.
+constexpr int kBoost = 8;
+
+template <int D, int NC, int PIECES, typename TQ, typename TO>
+__global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, int column_tiles, int splits) {
+    constexpr int KW = D / 32, VN = D == 64 ? 4 : 8, VW = KvTile<D>::VW;
+    constexpr int LD = D + 4;  // floats a column in LDS
+    __shared__ float part[4][16][LD];
+    __shared__ float stat[4][NC * 16][4];  // per wavefront and column: m, l, factor
+    const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int x = blockIdx.x;
+    const int split = x % splits;
+    x /= splits;
+    const int head = x % c.Hkv;
+    x /= c.Hkv;
+    const int b = x % c.B;
+    const KvSeq s = kv_seq(c, b);
+    const int columns = s.n * a.group;  // rows * Hq fits 31 bits
+    const int pos0 = s.len - s.n;
+    for (int ct = x / c.B; (int64_t)ct * 16 * NC < columns; ct += column_tiles) {
+        const int col0 = ct * 16 * NC, col1 = min(col0 + 16 * NC, columns) - 1;
+        const int p_lo = pos0 + col0 / a.group, p_hi = pos0 + col1 / a.group;
+        const int low_any = a.window > 0 ? max(p_lo, 0) - a.window : -1;
+        const KvWalk walk = kv_walk(p_lo, p_hi, a.window, a.sinks);
+        const int j1 = (int)((int64_t)walk.count * (split + 1) / splits);
+        int j = (int)((int64_t)walk.count * split / splits) + wave;
+
+        KvTile<D> cur, next;
+        auto fetch = [&](KvTile<D>& t, int jj) {
+            KvHalf h[2];
+            const int t0 = walk.tile(jj) * 32;
+            h[0] = kv_half(c, b, head, t0);
+            h[1] = kv_half(c, b, head, t0 + 16);
+            if (jj >= j1) h[0].n = h[1].n = 0;  // past the end: reads nothing
+            t.load(c, h, lane);
+        };
+        fetch(cur, j);
+
+        // the columns' queries and positions
+        KvQuery<D, PIECES> q[NC];
+        int pos[NC], low[NC];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            const int col = col0 + 16 * n + l16;
+            const bool live = col < columns;
+            const int row = live ? col / a.group : 0, h = live ? col - row * a.group : 0;
+            const TQ* p = static_cast<const TQ*>(a.q) + (int64_t)(s.first + row) * a.q_row +
+                          (int64_t)(head * a.group + h) * a.q_head + g * (D / 4);
+            q[n].load(p, live, a.scale);
+            pos[n] = live ? pos0 + row : -1;
+            low[n] = a.window > 0 ? max(pos[n], 0) - a.window : -1;
+        }
+        float mx[NC], thr[NC], l[NC];
+        f32v4_t o[NC][VW * VN];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            thr[n] = -INFINITY;  // nothing seen so far
+            mx[n] = l[n] = 0.f;
+#pragma unroll
+            for (int i = 0; i < VW * VN; ++i) o[n][i] = f32v4_t{0.f, 0.f, 0.f, 0.f};
+        }
+        float rv = 0.f, sv_max = 0.f;  // 2^(kBoost - e), 8 * 2^e
+
+        for (; j < j1; j += 4) {
+            const int t0 = walk.tile(j) * 32;
+            const KvHalf h0 = kv_half(c, b, head, t0), h1 = kv_half(c, b, head, t0 + 16);
+            fetch(next, j + 4);
+            // scores
+            f32v4_t z[NC][2];
+#pragma unroll
+            for (int n = 0; n < NC; ++n) z[n][0] = z[n][1] = f32v4_t{q[n].zero, q[n].zero, q[n].zero, q[n].zero};
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int w = 0; w < KW; ++w) {
+                    const f16x8_t k = nibbles_a(cur.k[h][w]);
+#pragma unroll
+                    for (int n = 0; n < NC; ++n)
+#pragma unroll
+                        for (int p = 0; p < PIECES; ++p) z[n][h] = mfma16(k, q[n].f[p][w], z[n][h]);
+                }
+            // masks where the tile needs them: the rows' ends, the window's, the pages'
+            const bool whole = h0.n == 16 && h1.n == 16;
+            const bool seen = whole && t0 + 31 <= p_lo &&
+                              (a.window == 0 || t0 > max(p_hi, 0) - a.window || t0 + 31 < a.sinks);
+            float top[NC];
+            if (!seen) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int idx = 4 * g + r, t = t0 + 16 * h + idx;
+                        // a scale that no column sees may be stale: any bits
+                        const bool there = idx < (h ? h1.n : h0.n) && t <= p_hi && (t > low_any || t < a.sinks);
+                        cur.sk[h][r] = there ? cur.sk[h][r] : 0.f;
+                        cur.sv[h][r] = there ? cur.sv[h][r] : 0.f;
+#pragma unroll
+                        for (int n = 0; n < NC; ++n) {
+                            const bool see = there && t <= pos[n] && (t > low[n] || t < a.sinks);
+                            z[n][h][r] = see ? fmaf(z[n][h][r], cur.sk[h][r], -mx[n]) : -INFINITY;
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int n = 0; n < NC; ++n) z[n][h][r] = fmaf(z[n][h][r], cur.sk[h][r], -mx[n]);
+            }
+            // references: rarely moved
+            bool move = false;
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+                top[n] = z[n][0][0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) top[n] = fmaxf(top[n], z[n][i >> 2][i & 3]);
+                move = move || top[n] > thr[n];
+            }
+            float big = cur.sv[0][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) big = fmaxf(big, cur.sv[i >> 2][i & 3]);
+            if (__builtin_amdgcn_ballot_w64(move || big >= sv_max) != 0) {
+                float fv = 1.f;
+                big = wave_max(big);
+                if (big >= sv_max && big > 0.f) {
+                    const int e = min(max(ilogbf(big), -110), 110);
+                    const float r = ldexpf(1.f, kBoost - e);
+                    fv = rv > 0.f ? r / rv : 0.f;  // powers of two
+                    rv = r;
+                    sv_max = ldexpf(8.f, e);
+                }
+#pragma unroll
+                for (int n = 0; n < NC; ++n) {
+                    float t = fmaxf(top[n], __shfl_xor(top[n], 16));
+                    t = fmaxf(t, __shfl_xor(t, 32));
+                    float f = 1.f;
+                    if (t > thr[n]) {  // alike on the column's four lanes
+                        const float to = mx[n] + t, by = to - mx[n];
+                        f = thr[n] > -INFINITY ? __builtin_amdgcn_exp2f(-by * q[n].c) : 0.f;
+                        mx[n] = to;
+                        thr[n] = kLift / q[n].c;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) z[n][i >> 2][i & 3] -= by;
+                    }
+                    l[n] *= f;
+                    f *= fv;
+#pragma unroll
+                    for (int i = 0; i < VW * VN; ++i) o[n][i] *= f;
+                }
+            }
+            // weights, and their operands of the second product
+            f32v4_t sv[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) sv[h] = cur.sv[h] * rv;
+            f16x8_t pf[NC][PIECES];
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    float y[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float p = __builtin_amdgcn_exp2f(z[n][(i + u) >> 2][(i + u) & 3] * q[n].c);
+                        l[n] += p;
+                        y[u] = p * sv[(i + u) >> 2][(i + u) & 3];
+                    }
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p) {
+                        const f16x2_t v = {(_Float16)y[0], (_Float16)y[1]};
+                        pf[n][p][i] = v[0];
+                        pf[n][p][i + 1] = v[1];
+                        y[0] -= (float)v[0];
+                        y[1] -= (float)v[1];
+                    }
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+                uint32_t words[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) words[i] = cur.v[i][w];
+                f16x8_t vf[VN];
+                nibble_columns(words, vf);
+#pragma unroll
+                for (int i = 0; i < VN; ++i)
+#pragma unroll
+                    for (int n = 0; n < NC; ++n)
+#pragma unroll
+                        for (int p = 0; p < PIECES; ++p) o[n][w * VN + i] = mfma16(vf[i], pf[n][p], o[n][w * VN + i]);
+            }
+            cur = next;
+        }
+
+        // the wavefronts' references and sums
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            l[n] += __shfl_xor(l[n], 16);
+            l[n] += __shfl_xor(l[n], 32);
+            if (g == 0) {
+                stat[wave][16 * n + l16][0] = thr[n] > -INFINITY ? mx[n] * q[n].c : -INFINITY;
+                stat[wave][16 * n + l16][1] = l[n];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) top = fmaxf(top, stat[w][16 * n + l16][0]);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float mw = stat[w][16 * n + l16][0];
+                sum += mw > -INFINITY ? stat[w][16 * n + l16][1] * __builtin_amdgcn_exp2f(mw - top) : 0.f;
+            }
+            // this wavefront's share of the columns, d consecutive per lane
+            const float f = thr[n] > -INFINITY && rv > 0.f ? __builtin_amdgcn_exp2f(mx[n] * q[n].c - top) / rv : 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < VW * VN; i += 4)
+                    *reinterpret_cast<f32v4_t*>(&part[wave][l16][(4 * g + r) * (VW * VN) + i]) =
+                        f32v4_t{o[n][i][r], o[n][i + 1][r], o[n][i + 2][r], o[n][i + 3][r]} * f;
+            __syncthreads();
+            // 16 threads a column add the four and store
+            const int cl = threadIdx.x >> 4, col = col0 + 16 * n + cl;
+            constexpr int E = D / 16;
+            const int e0 = (threadIdx.x & 15) * E;
+            float y[E];
+#pragma unroll
+            for (int i = 0; i < E; i += 4) {
+                const f32v4_t v = (*reinterpret_cast<const f32v4_t*>(&part[0][cl][e0 + i]) +
+                                   *reinterpret_cast<const f32v4_t*>(&part[1][cl][e0 + i])) +
+                                  (*reinterpret_cast<const f32v4_t*>(&part[2][cl][e0 + i]) +
+                                   *reinterpret_cast<const f32v4_t*>(&part[3][cl][e0 + i]));
+#pragma unroll
+                for (int u = 0; u < 4; ++u) y[i + u] = v[u];
+            }
+            // top and sum of column l16 are those of column cl on the threads that store it
+            const float ctop = __shfl(top, cl), csum = __shfl(sum, cl);
+            if (col < columns) {
+                const int row = s.first + col / a.group, h = head * a.group + col % a.group;
+                if (splits > 1) {
+                    float* w = static_cast<float*>(a.work) +
+                               ((int64_t)row * a.Hq + h) * splits * kv_partial_floats(D) + (int64_t)split * kv_partial_floats(D);
+#pragma unroll
+                    for (int i = 0; i < E; i += 4)
+                        *reinterpret_cast<f32v4_t*>(w + e0 + i) = f32v4_t{y[i], y[i + 1], y[i + 2], y[i + 3]};
+                    if (e0 == 0) *reinterpret_cast<f32v4_t*>(w + D) = f32v4_t{ctop, csum, 0.f, 0.f};
+                } else {
+                    const float inv = csum > 0.f ? 1.f / csum : 0.f;
+#pragma unroll
+                    for (int i = 0; i < E; ++i) y[i] *= inv;
+                    store_run<E>(static_cast<TO*>(a.out) + row * a.out_row + h * a.out_head + e0, y);
+                    if (a.lse && e0 == 0)
+                        a.lse[(int64_t)row * a.Hq + h] = csum > 0.f ? (ctop + __builtin_amdgcn_logf(csum)) * 0.6931471805599453f : -INFINITY;
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// Partial results of the parts: one wavefront a (row, query head).
+template <int D, typename TO>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvPages c, KvAttn a, int splits) {
+    constexpr int PF = D + 4, E = D / 64;
+    const int lane = threadIdx.x & 63;
+    const int64_t v = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (v >= (int64_t)c.rows * a.Hq) return;  // whole wavefront
+    const int row = (int)(v / a.Hq), h = (int)(v - (int64_t)row * a.Hq);
+    // rows of no sequence have no partial results
+    if (c.starts && (row < c.starts[0] || row >= c.starts[c.B])) return;
+    const float* w = static_cast<const float*>(a.work) + v * splits * PF;
+    float top = -INFINITY;
+    for (int i = lane; i < splits; i += 64) top = fmaxf(top, w[(int64_t)i * PF + D]);
+    top = wave_max(top);
+    float sum = 0.f, y[E] = {};
+    for (int i = 0; i < splits; ++i) {
+        const float m = w[(int64_t)i * PF + D];
+        if (m == -INFINITY) continue;
+        const float f = __builtin_amdgcn_exp2f(m - top);
+        sum = fmaf(w[(int64_t)i * PF + D + 1], f, sum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = fmaf(w[(int64_t)i * PF + lane * E + e], f, y[e]);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] *= inv;
+    store_run<E>(static_cast<TO*>(a.out) + row * a.out_row + h * a.out_head + lane * E, y);
+    if (a.lse && lane == 0) a.lse[v] = sum > 0.f ? (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+// ---------------------------------------------------------------- host side
+template <int D, int NC, int PIECES, typename TQ, typename TO>
+hipError_t launch_kv_split_as(const KvPages& c, const KvAttn& a, const KvPlan& p, hipStream_t st) {
+    const int64_t blocks = (int64_t)p.column_tiles * c.B * c.Hkv * p.splits;
+    hipLaunchKernelGGL((kv_split_kernel<D, NC, PIECES, TQ, TO>), dim3((unsigned)blocks), dim3(256), 0, st, c, a,
+                       p.column_tiles, p.splits);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1) return e;
+    hipLaunchKernelGGL((kv_join_kernel<D, TO>), dim3((unsigned)(((int64_t)c.rows * a.Hq + 3) / 4)), dim3(256), 0, st,
+                       c, a, p.splits);
+    return hipGetLastError();
+}
+
+template <int D, int PIECES>
+hipError_t launch_kv_split(const KvPages& c, const KvAttn& a, bool q_bf16, bool out_bf16, hipStream_t st) {
+    const KvPlan p = kv_plan(c, D, a.group, a.max_rows, a.max_len, a.window, a.sinks);
+    auto go = [&](auto nc) -> hipError_t {
+        constexpr int NC = decltype(nc)::value;
+        if constexpr (PIECES == 1) return launch_kv_split_as<D, NC, 1, __bf16, __bf16>(c, a, p, st);
+        else if (!q_bf16 && !out_bf16) return launch_kv_split_as<D, NC, 2, float, float>(c, a, p, st);
+        else if (!q_bf16) return launch_kv_split_as<D, NC, 2, float, __bf16>(c, a, p, st);
+        else return launch_kv_split_as<D, NC, 2, __bf16, float>(c, a, p, st);
+    };
+    if constexpr (D < 256)
+        if (p.nc == 2) return go(std::integral_constant<int, 2>{});
+    return go(std::integral_constant<int, 1>{});
+}
+
+}  // namespace w4

@@ -7,6 +7,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "common.hpp"
+
 namespace w4 {
 
 struct KvPages {  // passed to kernels by value
@@ -70,6 +72,35 @@ __device__ __forceinline__ void load8(const __bf16* p, float* v) {
     for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(w[i] << 16);
         v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+// E consecutive results of a row tensor, E * sizeof(T) bytes aligned.
+template <int E> __device__ __forceinline__ void store_run(float* p, const float* v) {
+    if constexpr (E % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < E; i += 4)
+            reinterpret_cast<float4*>(p)[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) p[i] = v[i];
+    }
+}
+template <int E> __device__ __forceinline__ void store_run(__bf16* p, const float* v) {
+    uint32_t w[(E + 1) / 2];
+#pragma unroll
+    for (int i = 0; i < (E + 1) / 2; ++i)
+        w[i] = f32_to_bf16_rne(v[2 * i]) | (2 * i + 1 < E ? f32_to_bf16_rne(v[2 * i + 1]) << 16 : 0u);
+    if constexpr (E % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < E / 2; i += 4)
+            reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    } else if constexpr (E == 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else if constexpr (E == 2) {
+        *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else {
+        *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
     }
 }
 

@@ -79,17 +79,6 @@ __global__ __launch_bounds__(256) void kv_write_kernel(KvPages c, KvRowsArg a, i
     }
 }
 
-__device__ __forceinline__ void store8(float* p, const float* v) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(__bf16* p, const float* v) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16_rne(v[2 * i]) | (f32_to_bf16_rne(v[2 * i + 1]) << 16);
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 template <int D, typename T>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvPages c, KvRowsArg a, int chunks) {
     constexpr int LANES = D / 8, VECS = 256 / LANES;
@@ -110,7 +99,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvPages c, KvRowsArg a, in
         float e[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] = (float)((int)((w >> (4 * i)) & 15u) - 8) * sc;
-        store8(static_cast<T*>(a.data[kv]) + p.row * a.row_stride[kv] + p.head * a.head_stride[kv] + 8 * l, e);
+        store_run<8>(static_cast<T*>(a.data[kv]) + p.row * a.row_stride[kv] + p.head * a.head_stride[kv] + 8 * l, e);
     }
 }
 

@@ -108,8 +108,9 @@ def kv_attention(q, k, v, scale, window=0, sinks=0):
     q [n][Hq][D]; k, v [Hkv][L][D]; row i stands at position L - n + i and sees t <= its position,
     with window > 0 only t > position - window or t < sinks. Hidden keys' values do not enter, whatever
     they are. Returns out [n][Hq][D], lse [n][Hq], and what tolerances are made of: A [n][Hq][D] =
-    sum_t p_t |v_t|, Z [n][Hq] = max over visible t of scale * sum_i |q_i||k_ti|, and Zmax [n][Hq] = the
-    same with max|q| for every |q_i|. A row that sees nothing: out 0, lse -inf, the rest 0."""
+    sum_t p_t |v_t|, Z [n][Hq] = max over visible t of |scale| * sum_i |q_i| (|k_ti| + 8/7 max_i |k_ti|) (a
+    key's largest code is 7 or -8, so 8/7 of its largest value is 8 scales at least: Z covers the sums
+    over codes stored plus 8), and Zmax [n][Hq] = the same with max|q| for every |q_i|. A row that sees nothing: out 0, lse -inf, the rest 0."""
     q = np.asarray(q, dtype=np.float64)
     n, Hq, D = q.shape
     L = k.shape[1]
@@ -132,6 +133,7 @@ def kv_attention(q, k, v, scale, window=0, sinks=0):
             out[i, h] = e @ V / e.sum()
             A[i, h] = e @ np.abs(V) / e.sum()
             lse[i, h] = m + np.log(e.sum())
-            Z[i, h] = (abs(scale) * (np.abs(K) @ np.abs(x))).max()
-            Zmax[i, h] = (abs(scale) * np.abs(K).sum(1) * np.abs(x).max()).max()
+            K8 = np.abs(K) + 8 / 7 * np.abs(K).max(axis=1, keepdims=True)
+            Z[i, h] = (abs(scale) * (K8 @ np.abs(x))).max()
+            Zmax[i, h] = (abs(scale) * K8.sum(1) * np.abs(x).max()).max()
     return out, lse, A, Z, Zmax

@@ -98,8 +98,9 @@ def bounds(ref, D, L, vmax, q_dtype, out_dtype):
 
     Scores. A bf16 query is exact in the 16-bit format of the products but for what falls under its
     least step, 2^-25 of the row's maximum < u max|q|; an fp32 one goes in two pieces of 11 bits, off
-    by 2^-22 |q| = 4 u |q| at most. Products with the integer codes are exact, their 2 D terms (two
-    pieces) add up in fp32 to 2 D u, the two scalings to 4 u, the exponent's argument to 4 u (Z + |m|) with
+    by 2^-22 |q| = 4 u |q| at most. Products with the integer codes (stored plus 8, the offset's part a
+    term of its own: Z and Zmax count both) are exact, their 2 D terms (two pieces) add up in fp32 to
+    2 D u, the scalings to 4 u, the exponent's argument to 4 u (Z + |m|) with
     the running maximum m, |m| <= Z, and the exponential is good to 2^-22:
         dz = u (Zmax + (2 D + 16) Z) + 2^-22.
     Weights. e^z is off by w = e^(2 dz) - 1 (a row's weight and its maximum's), and sums of L terms by

@@ -97,6 +97,21 @@ def test_attention_refusals():
     assert _attend(p, b, q, q, lse=24, **big) == -3
 
 
+def test_attention_workspace():
+    """Few sequences over a long cache split their keys and need a workspace, whose absence is refused."""
+    L = w4.lib()
+    p, b, q = _pages(page_size=4096, num_pages=64), _batch(width=32, stride=32), _rows(rs=512)
+    need = L.w4_kv_attention_workspace_bytes(ctypes.byref(p), ctypes.byref(b), 4, 0, 0)
+    assert need > 0
+    assert _attend(p, b, q, q) == -5 and _attend(p, b, q, q, ws=16, nbytes=need - 1) == -5
+    assert b"workspace" in L.w4_last_error()
+    assert _attend(p, b, q, q, ws=8, nbytes=need) == -3
+    # a window leaves little to split; a bound on the lengths as well
+    assert L.w4_kv_attention_workspace_bytes(ctypes.byref(p), ctypes.byref(b), 4, 64, 4) < need
+    short = _batch(width=32, stride=32, max_len=100)
+    assert L.w4_kv_attention_workspace_bytes(ctypes.byref(p), ctypes.byref(short), 4, 0, 0) < need
+
+
 def test_oracle_attention_against_closed_forms():
     rng = np.random.default_rng(0)
     v = rng.standard_normal((2, 9, 4))
