@@ -17,7 +17,7 @@ KvPlan kv_plan(const KvPages& c, int D, int group, int64_t max_rows, int64_t max
     const int64_t columns = max_rows * group;
     p.nc = columns > 16 && D < 256 ? 2 : 1;
     const int64_t tiles = (columns + 16 * p.nc - 1) / (16 * p.nc);
-    const int64_t most = 0x7fffffffLL / ((int64_t)c.B * c.Hkv);  // longer sequences loop
+    const int64_t most = 0x7fffffLL / c.B;  // longer sequences loop
     p.column_tiles = (int)(tiles < most ? tiles : most);
     // the keys that a tile of columns walks over, in tiles of 32
     int64_t keys = max_len;
@@ -27,11 +27,20 @@ KvPlan kv_plan(const KvPages& c, int D, int group, int64_t max_rows, int64_t max
         keys = window + rows + (sinks < rest ? sinks : rest) + 64;
     }
     const int64_t key_tiles = (keys + 31) / 32;
+    // Parts of the keys: rounds of workgroups over the chip (3 a CU fit its registers, 2 of
+    // the wider kernels), each as long as a wavefront's share of the tiles and what a
+    // workgroup costs besides, about two tiles' time, as does the launch that joins them. Measured with 8 kv heads: a batch of 48
+    // of up to 8192 positions (384 workgroups a part) 77 us whole, 50 in two parts (one round),
+    // 58 in three, 62 in eight; two sequences of 131072 (16) 52 us in 48 parts, 67 in 16.
     const int64_t blocks = (int64_t)p.column_tiles * c.B * c.Hkv;
-    int64_t s = (1024 + blocks - 1) / blocks;      // workgroups for every CU
-    const int64_t cap = (key_tiles + 7) / 8;       // two tiles a wavefront at least
-    s = s < cap ? s : cap;
-    p.splits = (int)(s < 1 ? 1 : s > 256 ? 256 : s);
+    const int64_t fit = 256 * (p.nc == 1 && D < 256 ? 3 : 2);
+    const int64_t cap = key_tiles < 4 * kMaxSplits ? (key_tiles + 3) / 4 : kMaxSplits;
+    int64_t best = 0;
+    p.splits = 1;
+    for (int64_t s = 1; s <= cap && (s == 1 || blocks * s <= 8 * fit); ++s) {
+        const int64_t cost = (blocks * s + fit - 1) / fit * ((key_tiles + 4 * s - 1) / (4 * s) + 2) + (s > 1 ? 2 : 0);
+        if (s == 1 || cost < best) best = cost, p.splits = (int)s;
+    }
     return p;
 }
 

@@ -24,12 +24,13 @@ struct KvPlan {
     int nc;            // 16-column tiles a workgroup takes at once
     int splits;        // parts of a sequence's keys
 };
+constexpr int kMaxSplits = 64;
 KvPlan kv_plan(const KvPages& c, int D, int group, int64_t max_rows, int64_t max_len, int64_t window,
                int64_t sinks);
 
 // Partial results of a part: out[D] unnormalized, then the exponent's reference
 // (base 2) and the sum.
-__host__ __device__ inline int kv_partial_floats(int D) { return D + 4; }
+__host__ __device__ constexpr int kv_partial_floats(int D) { return D + 4; }
 inline size_t kv_partial_bytes(int64_t vectors, int splits, int D) {
     return (size_t)vectors * splits * kv_partial_floats(D) * sizeof(float);
 }
@@ -47,54 +48,83 @@ constexpr float kLift = 4.f;
 constexpr int kBoost = 8;
 
 template <int D, int NC, int PIECES, typename TQ, typename TO>
-__global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, int column_tiles, int splits) {
-    constexpr int KW = D / 32, VN = D == 64 ? 4 : 8, VW = KvTile<D>::VW;
+__global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_kernel(KvPages c, KvAttn a, int column_tiles, int splits) {
+    constexpr int KW = D / 32, VN = D == 64 ? 4 : 8, VW = KvValues<D>::VW;
     constexpr int LD = D + 4;  // floats a column in LDS
-    __shared__ float part[4][16][LD];
-    __shared__ float stat[4][NC * 16][4];  // per wavefront and column: m, l, factor
+    constexpr bool HOLD = PIECES * KW * NC <= 4;  // queries in registers, else read from LDS for every tile
+    union Lds {
+        KvQueries<D, NC, PIECES> q;
+        float part[4][16][LD];  // after the last tile
+    };
+    __shared__ __align__(16) char lds_raw[sizeof(Lds)];
+    Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
+    __shared__ float q_zero[16 * NC], q_c[16 * NC];
+    __shared__ float stat[4][NC * 16][2];  // per wavefront and column: reference, sum
     const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int x = blockIdx.x;
-    const int split = x % splits;
-    x /= splits;
-    const int head = x % c.Hkv;
-    x /= c.Hkv;
-    const int b = x % c.B;
+    const int split = blockIdx.z, head = blockIdx.y, b = blockIdx.x / column_tiles;
     const KvSeq s = kv_seq(c, b);
     const int columns = s.n * a.group;  // rows * Hq fits 31 bits
     const int pos0 = s.len - s.n;
-    for (int ct = x / c.B; (int64_t)ct * 16 * NC < columns; ct += column_tiles) {
+    const KvTable table(c, b);
+    for (int ct = blockIdx.x - b * column_tiles; (int64_t)ct * 16 * NC < columns; ct += column_tiles) {
         const int col0 = ct * 16 * NC, col1 = min(col0 + 16 * NC, columns) - 1;
         const int p_lo = pos0 + col0 / a.group, p_hi = pos0 + col1 / a.group;
         const int low_any = a.window > 0 ? max(p_lo, 0) - a.window : -1;
         const KvWalk walk = kv_walk(p_lo, p_hi, a.window, a.sinks);
-        const int j1 = (int)((int64_t)walk.count * (split + 1) / splits);
-        int j = (int)((int64_t)walk.count * split / splits) + wave;
+        // count < 2^26 and splits <= 64: 32 bits hold the products
+        const int j1 = (int)((unsigned)walk.count * (unsigned)(split + 1) / (unsigned)splits);
+        int j = (int)((unsigned)walk.count * (unsigned)split / (unsigned)splits) + wave;
 
-        KvTile<D> cur, next;
-        auto fetch = [&](KvTile<D>& t, int jj) {
-            KvHalf h[2];
-            const int t0 = walk.tile(jj) * 32;
-            h[0] = kv_half(c, b, head, t0);
-            h[1] = kv_half(c, b, head, t0 + 16);
-            if (jj >= j1) h[0].n = h[1].n = 0;  // past the end: reads nothing
-            t.load(c, h, lane);
+        // One tile's registers: the next tile's keys are loaded once the scores are
+        // formed, its values once the second product is, its page table entries a
+        // step before. The other wavefronts of the SIMD cover the rest.
+        KvKeys<D> keys;
+        KvValues<D> vals;
+        KvHalf half[2];
+        int entry[2];
+        auto entries = [&](int jj) {
+            const int t0 = walk.tile(min(jj, j1)) * 32;
+            entry[0] = table.entry(t0);
+            entry[1] = table.entry(t0 + 16);
         };
-        fetch(cur, j);
+        auto locate = [&](int jj) {
+            const int t0 = walk.tile(min(jj, j1)) * 32;
+            half[0] = kv_half(c, b, head, t0, entry[0]);
+            half[1] = kv_half(c, b, head, t0 + 16, entry[1]);
+            if (jj >= j1) half[0].n = half[1].n = 0;  // past the end: reads nothing
+        };
+        entries(j);
+        locate(j);
+        keys.load(c, half, lane);
+        vals.load(c, half, lane);
+        entries(j + 4);
 
-        // the columns' queries and positions
-        KvQuery<D, PIECES> q[NC];
+        make_queries<D, NC, PIECES>(lds.q, q_zero, q_c, a.scale, [&](int i) -> const TQ* {
+            const int col = col0 + i, row = col / a.group;
+            return col < columns ? static_cast<const TQ*>(a.q) + (int64_t)(s.first + row) * a.q_row +
+                                       (int64_t)(head * a.group + col - row * a.group) * a.q_head
+                                 : nullptr;
+        });
+        __syncthreads();
+        f16x8_t q[HOLD ? PIECES : 1][HOLD ? NC : 1][HOLD ? KW : 1];
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+                for (int n = 0; n < NC; ++n)
+#pragma unroll
+                    for (int w = 0; w < KW; ++w) q[p][n][w] = lds.q.frag[p][n][w][lane];
+        }
         int pos[NC], low[NC];
+        float qz[NC], qc[NC];
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
             const int col = col0 + 16 * n + l16;
-            const bool live = col < columns;
-            const int row = live ? col / a.group : 0, h = live ? col - row * a.group : 0;
-            const TQ* p = static_cast<const TQ*>(a.q) + (int64_t)(s.first + row) * a.q_row +
-                          (int64_t)(head * a.group + h) * a.q_head + g * (D / 4);
-            q[n].load(p, live, a.scale);
-            pos[n] = live ? pos0 + row : -1;
+            pos[n] = col < columns ? pos0 + col / a.group : -1;
             low[n] = a.window > 0 ? max(pos[n], 0) - a.window : -1;
+            qz[n] = q_zero[16 * n + l16];
+            qc[n] = q_c[16 * n + l16];
         }
         float mx[NC], thr[NC], l[NC];
         f32v4_t o[NC][VW * VN];
@@ -109,24 +139,25 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
 
         for (; j < j1; j += 4) {
             const int t0 = walk.tile(j) * 32;
-            const KvHalf h0 = kv_half(c, b, head, t0), h1 = kv_half(c, b, head, t0 + 16);
-            fetch(next, j + 4);
+            int at = lane;  // opaque, so that queries read from LDS stay there
+            if constexpr (!HOLD) asm volatile("" : "+v"(at));
             // scores
             f32v4_t z[NC][2];
 #pragma unroll
-            for (int n = 0; n < NC; ++n) z[n][0] = z[n][1] = f32v4_t{q[n].zero, q[n].zero, q[n].zero, q[n].zero};
+            for (int n = 0; n < NC; ++n) z[n][0] = z[n][1] = f32v4_t{qz[n], qz[n], qz[n], qz[n]};
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int w = 0; w < KW; ++w) {
-                    const f16x8_t k = nibbles_a(cur.k[h][w]);
+                    const f16x8_t k = nibbles_a(keys.w[h][w]);
 #pragma unroll
                     for (int n = 0; n < NC; ++n)
 #pragma unroll
-                        for (int p = 0; p < PIECES; ++p) z[n][h] = mfma16(k, q[n].f[p][w], z[n][h]);
+                        for (int p = 0; p < PIECES; ++p)
+                            z[n][h] = mfma16(k, HOLD ? q[HOLD ? p : 0][HOLD ? n : 0][HOLD ? w : 0] : lds.q.frag[p][n][w][at], z[n][h]);
                 }
             // masks where the tile needs them: the rows' ends, the window's, the pages'
-            const bool whole = h0.n == 16 && h1.n == 16;
+            const bool whole = half[0].n == 16 && half[1].n == 16;
             const bool seen = whole && t0 + 31 <= p_lo &&
                               (a.window == 0 || t0 > max(p_hi, 0) - a.window || t0 + 31 < a.sinks);
             float top[NC];
@@ -137,13 +168,13 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
                     for (int r = 0; r < 4; ++r) {
                         const int idx = 4 * g + r, t = t0 + 16 * h + idx;
                         // a scale that no column sees may be stale: any bits
-                        const bool there = idx < (h ? h1.n : h0.n) && t <= p_hi && (t > low_any || t < a.sinks);
-                        cur.sk[h][r] = there ? cur.sk[h][r] : 0.f;
-                        cur.sv[h][r] = there ? cur.sv[h][r] : 0.f;
+                        const bool there = idx < half[h].n && t <= p_hi && (t > low_any || t < a.sinks);
+                        keys.scale[h][r] = there ? keys.scale[h][r] : 0.f;
+                        vals.scale[h][r] = there ? vals.scale[h][r] : 0.f;
 #pragma unroll
                         for (int n = 0; n < NC; ++n) {
                             const bool see = there && t <= pos[n] && (t > low[n] || t < a.sinks);
-                            z[n][h][r] = see ? fmaf(z[n][h][r], cur.sk[h][r], -mx[n]) : -INFINITY;
+                            z[n][h][r] = see ? fmaf(z[n][h][r], keys.scale[h][r], -mx[n]) : -INFINITY;
                         }
                     }
             } else {
@@ -152,8 +183,11 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
 #pragma unroll
-                        for (int n = 0; n < NC; ++n) z[n][h][r] = fmaf(z[n][h][r], cur.sk[h][r], -mx[n]);
+                        for (int n = 0; n < NC; ++n) z[n][h][r] = fmaf(z[n][h][r], keys.scale[h][r], -mx[n]);
             }
+            locate(j + 4);
+            keys.load(c, half, lane);
+            entries(j + 8);
             // references: rarely moved
             bool move = false;
 #pragma unroll
@@ -163,9 +197,9 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
                 for (int i = 1; i < 8; ++i) top[n] = fmaxf(top[n], z[n][i >> 2][i & 3]);
                 move = move || top[n] > thr[n];
             }
-            float big = cur.sv[0][0];
+            float big = vals.scale[0][0];
 #pragma unroll
-            for (int i = 1; i < 8; ++i) big = fmaxf(big, cur.sv[i >> 2][i & 3]);
+            for (int i = 1; i < 8; ++i) big = fmaxf(big, vals.scale[i >> 2][i & 3]);
             if (__builtin_amdgcn_ballot_w64(move || big >= sv_max) != 0) {
                 float fv = 1.f;
                 big = wave_max(big);
@@ -183,9 +217,9 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
                     float f = 1.f;
                     if (t > thr[n]) {  // alike on the column's four lanes
                         const float to = mx[n] + t, by = to - mx[n];
-                        f = thr[n] > -INFINITY ? __builtin_amdgcn_exp2f(-by * q[n].c) : 0.f;
+                        f = thr[n] > -INFINITY ? __builtin_amdgcn_exp2f(-by * qc[n]) : 0.f;
                         mx[n] = to;
-                        thr[n] = kLift / q[n].c;
+                        thr[n] = kLift / qc[n];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) z[n][i >> 2][i & 3] -= by;
                     }
@@ -198,7 +232,7 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
             // weights, and their operands of the second product
             f32v4_t sv[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) sv[h] = cur.sv[h] * rv;
+            for (int h = 0; h < 2; ++h) sv[h] = vals.scale[h] * rv;
             f16x8_t pf[NC][PIECES];
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
@@ -207,7 +241,7 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
                     float y[2];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const float p = __builtin_amdgcn_exp2f(z[n][(i + u) >> 2][(i + u) & 3] * q[n].c);
+                        const float p = __builtin_amdgcn_exp2f(z[n][(i + u) >> 2][(i + u) & 3] * qc[n]);
                         l[n] += p;
                         y[u] = p * sv[(i + u) >> 2][(i + u) & 3];
                     }
@@ -225,7 +259,7 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
             for (int w = 0; w < VW; ++w) {
                 uint32_t words[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) words[i] = cur.v[i][w];
+                for (int i = 0; i < 8; ++i) words[i] = vals.w[i][w];
                 f16x8_t vf[VN];
                 nibble_columns(words, vf);
 #pragma unroll
@@ -235,7 +269,7 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
 #pragma unroll
                         for (int p = 0; p < PIECES; ++p) o[n][w * VN + i] = mfma16(vf[i], pf[n][p], o[n][w * VN + i]);
             }
-            cur = next;
+            vals.load(c, half, lane);
         }
 
         // the wavefronts' references and sums
@@ -244,7 +278,7 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
             l[n] += __shfl_xor(l[n], 16);
             l[n] += __shfl_xor(l[n], 32);
             if (g == 0) {
-                stat[wave][16 * n + l16][0] = thr[n] > -INFINITY ? mx[n] * q[n].c : -INFINITY;
+                stat[wave][16 * n + l16][0] = thr[n] > -INFINITY ? mx[n] * qc[n] : -INFINITY;
                 stat[wave][16 * n + l16][1] = l[n];
             }
         }
@@ -260,12 +294,12 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
                 sum += mw > -INFINITY ? stat[w][16 * n + l16][1] * __builtin_amdgcn_exp2f(mw - top) : 0.f;
             }
             // this wavefront's share of the columns, d consecutive per lane
-            const float f = thr[n] > -INFINITY && rv > 0.f ? __builtin_amdgcn_exp2f(mx[n] * q[n].c - top) / rv : 0.f;
+            const float f = thr[n] > -INFINITY && rv > 0.f ? __builtin_amdgcn_exp2f(mx[n] * qc[n] - top) / rv : 0.f;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int i = 0; i < VW * VN; i += 4)
-                    *reinterpret_cast<f32v4_t*>(&part[wave][l16][(4 * g + r) * (VW * VN) + i]) =
+                    *reinterpret_cast<f32v4_t*>(&lds.part[wave][l16][(4 * g + r) * (VW * VN) + i]) =
                         f32v4_t{o[n][i][r], o[n][i + 1][r], o[n][i + 2][r], o[n][i + 3][r]} * f;
             __syncthreads();
             // 16 threads a column add the four and store
@@ -275,10 +309,10 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
             float y[E];
 #pragma unroll
             for (int i = 0; i < E; i += 4) {
-                const f32v4_t v = (*reinterpret_cast<const f32v4_t*>(&part[0][cl][e0 + i]) +
-                                   *reinterpret_cast<const f32v4_t*>(&part[1][cl][e0 + i])) +
-                                  (*reinterpret_cast<const f32v4_t*>(&part[2][cl][e0 + i]) +
-                                   *reinterpret_cast<const f32v4_t*>(&part[3][cl][e0 + i]));
+                const f32v4_t v = (*reinterpret_cast<const f32v4_t*>(&lds.part[0][cl][e0 + i]) +
+                                   *reinterpret_cast<const f32v4_t*>(&lds.part[1][cl][e0 + i])) +
+                                  (*reinterpret_cast<const f32v4_t*>(&lds.part[2][cl][e0 + i]) +
+                                   *reinterpret_cast<const f32v4_t*>(&lds.part[3][cl][e0 + i]));
 #pragma unroll
                 for (int u = 0; u < 4; ++u) y[i + u] = v[u];
             }
@@ -307,42 +341,61 @@ __global__ __launch_bounds__(256, 2) void kv_split_kernel(KvPages c, KvAttn a, i
     }
 }
 
-// Partial results of the parts: one wavefront a (row, query head).
+// The parts of a (row, query head) meet: one wavefront each. Lane i holds part
+// i's reference and sum (kMaxSplits = 64 parts at most); D / 4 lanes share a
+// part's values, so 256 / D parts are read side by side, and kAhead loads a
+// lane are in flight before the references are known.
 template <int D, typename TO>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvPages c, KvAttn a, int splits) {
-    constexpr int PF = D + 4, E = D / 64;
+    constexpr int PF = kv_partial_floats(D), LANES = D / 4, SIDE = 64 / LANES, kAhead = 8;
     const int lane = threadIdx.x & 63;
     const int64_t v = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (v >= (int64_t)c.rows * a.Hq) return;  // whole wavefront
     const int row = (int)(v / a.Hq), h = (int)(v - (int64_t)row * a.Hq);
-    // rows of no sequence have no partial results
-    if (c.starts && (row < c.starts[0] || row >= c.starts[c.B])) return;
     const float* w = static_cast<const float*>(a.work) + v * splits * PF;
-    float top = -INFINITY;
-    for (int i = lane; i < splits; i += 64) top = fmaxf(top, w[(int64_t)i * PF + D]);
-    top = wave_max(top);
-    float sum = 0.f, y[E] = {};
-    for (int i = 0; i < splits; ++i) {
-        const float m = w[(int64_t)i * PF + D];
-        if (m == -INFINITY) continue;
-        const float f = __builtin_amdgcn_exp2f(m - top);
-        sum = fmaf(w[(int64_t)i * PF + D + 1], f, sum);
+    const int mine = min(lane, splits - 1), side = lane / LANES, e0 = 4 * (lane % LANES);
+    const f32v2_t ms = *reinterpret_cast<const f32v2_t*>(w + (int64_t)mine * PF + D);
+    f32v4_t x[kAhead];
+    auto load = [&](int base) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = fmaf(w[(int64_t)i * PF + lane * E + e], f, y[e]);
+        for (int k = 0; k < kAhead; ++k)
+            x[k] = *reinterpret_cast<const f32v4_t*>(w + (int64_t)min(base + SIDE * k + side, splits - 1) * PF + e0);
+    };
+    load(0);
+    // rows of no sequence have no parts
+    if (c.starts && (row < c.starts[0] || row >= c.starts[c.B])) return;
+    const float m = lane < splits ? ms[0] : -INFINITY;
+    const float top = wave_max(m);
+    const float f = m > -INFINITY ? __builtin_amdgcn_exp2f(m - top) : 0.f;
+    const float sum = group_sum<64>(f * ms[1]);
+    f32v4_t y = {0.f, 0.f, 0.f, 0.f};
+    for (int base = 0; base < splits; base += SIDE * kAhead) {
+        if (base) load(base);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = base + SIDE * k + side;
+            const float fi = __shfl(f, min(i, 63));
+            y += x[k] * (i < splits ? fi : 0.f);
+        }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] *= inv;
-    store_run<E>(static_cast<TO*>(a.out) + row * a.out_row + h * a.out_head + lane * E, y);
+    for (int o = LANES; o < 64; o <<= 1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += __shfl_xor(y[e], o);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (side == 0) {
+        const float r[4] = {y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv};
+        store_run<4>(static_cast<TO*>(a.out) + row * a.out_row + h * a.out_head + e0, r);
+    }
     if (a.lse && lane == 0) a.lse[v] = sum > 0.f ? (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 // ---------------------------------------------------------------- host side
 template <int D, int NC, int PIECES, typename TQ, typename TO>
 hipError_t launch_kv_split_as(const KvPages& c, const KvAttn& a, const KvPlan& p, hipStream_t st) {
-    const int64_t blocks = (int64_t)p.column_tiles * c.B * c.Hkv * p.splits;
-    hipLaunchKernelGGL((kv_split_kernel<D, NC, PIECES, TQ, TO>), dim3((unsigned)blocks), dim3(256), 0, st, c, a,
-                       p.column_tiles, p.splits);
+    const dim3 grid((unsigned)((int64_t)p.column_tiles * c.B), (unsigned)c.Hkv, (unsigned)p.splits);
+    hipLaunchKernelGGL((kv_split_kernel<D, NC, PIECES, TQ, TO>), grid, dim3(256), 0, st, c, a, p.column_tiles,
+                       p.splits);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     hipLaunchKernelGGL((kv_join_kernel<D, TO>), dim3((unsigned)(((int64_t)c.rows * a.Hq + 3) / 4)), dim3(256), 0, st,

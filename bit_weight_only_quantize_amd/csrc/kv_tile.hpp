@@ -24,6 +24,7 @@ namespace w4 {
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32v2_t __attribute__((ext_vector_type(2)));
 typedef float f32v4_t __attribute__((ext_vector_type(4)));
 typedef unsigned u32v4_t __attribute__((ext_vector_type(4)));
 typedef unsigned u32v2_t __attribute__((ext_vector_type(2)));
@@ -55,68 +56,82 @@ struct KvHalf {
 };
 typedef const int __attribute__((address_space(4)))* const_int_ptr;  // scalar loads
 
-__device__ __forceinline__ KvHalf kv_half(const KvPages& c, int b, int h, int t) {
-    KvHalf r;
-    int page = b, off = t;
-    bool good = t < c.capacity;
-    if (c.table) {
-        const int slot = good ? t >> c.page_shift : 0;
-        page = ((const_int_ptr)c.table)[b * c.table_stride + slot];
-        off = t & (c.page_size - 1);
-        good = good && (unsigned)page < (unsigned)c.num_pages;
+// The page table as one uniform walks it: entries are loaded well before they
+// are used, without a branch (no table: any word is loaded, and not looked at).
+struct KvTable {
+    const_int_ptr row;
+    int shift, last;  // of the positions
+    __device__ __forceinline__ KvTable(const KvPages& c, int b) {
+        row = (const_int_ptr)(c.table ? c.table + b * c.table_stride : c.lens);
+        shift = c.table ? c.page_shift : 31;
+        last = c.capacity - 1;
     }
+    __device__ __forceinline__ int entry(int t) const { return row[min(t, last) >> shift]; }
+};
+__device__ __forceinline__ KvHalf kv_half(const KvPages& c, int b, int h, int t, int entry) {
+    const int page = c.table ? entry : b;
+    const int off = c.table ? t & (c.page_size - 1) : t;
+    const bool good = t < c.capacity && (unsigned)page < (unsigned)c.num_pages;
+    KvHalf r;
     r.vec = good ? ((int64_t)page * c.Hkv + h) * c.page_size + off : 0;
     r.n = good ? min(16, c.page_size - off) : 0;
     return r;
 }
 
 // Raw contents of one tile on one wavefront.
-//   k[a][j]: word j of the lane's quarter of key 16 a + l % 16 (D / 32 words)
-//   v[i]: of key 16 a + 4 g + r (i = 4 a + r), the l % 16-th sixteenth of the
-//         vector: 4, 8 or 16 nibbles
-//   sk, sv[a]: the scales of keys 16 a + 4 g .. + 3
-template <int D> struct KvTile {
-    static constexpr int KW = D / 32;
-    static constexpr int VW = D == 256 ? 2 : 1;
-    uint32_t k[2][KW];
-    uint32_t v[8][VW];
-    f32v4_t sk[2], sv[2];
+//   keys: word j of the lane's quarter of key 16 a + l % 16 (D / 32 words)
+//   values: of key 16 a + 4 g + r (i = 4 a + r), the l % 16-th sixteenth of the
+//           vector: 4, 8 or 16 nibbles
+//   scale[a]: the scales of keys 16 a + 4 g .. + 3
+template <int D> struct KvKeys {
+    static constexpr int KW = D / 32, VB = D / 2;  // words a lane, bytes of a vector
+    uint32_t w[2][KW];
+    f32v4_t scale[2];
 
     __device__ __forceinline__ void load(const KvPages& c, const KvHalf* half, int lane) {
         const int l16 = lane & 15, g = lane >> 4;
-        constexpr int VB = D / 2;  // bytes of a vector
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-            const rsrc_t rs = make_rsrc(c.scales[0] + half[a].vec, half[a].n * 4);
             const rsrc_t rk = make_rsrc(c.codes[0] + half[a].vec * VB, half[a].n * VB);
-            sk[a] = __builtin_bit_cast(f32v4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * g, 0, 0));
             if constexpr (D == 64) {
-                const u32v2_t w = __builtin_amdgcn_raw_buffer_load_b64(rk, l16 * VB + 8 * g, 0, 0);
-                k[a][0] = w[0], k[a][1] = w[1];
+                const u32v2_t x = __builtin_amdgcn_raw_buffer_load_b64(rk, l16 * VB + 8 * g, 0, 0);
+                w[a][0] = x[0], w[a][1] = x[1];
             } else {
 #pragma unroll
                 for (int q = 0; q < KW / 4; ++q) {
-                    const u32v4_t w = __builtin_amdgcn_raw_buffer_load_b128(rk, l16 * VB + g * (VB / 4) + 16 * q, 0, 0);
+                    const u32v4_t x = __builtin_amdgcn_raw_buffer_load_b128(rk, l16 * VB + g * (VB / 4) + 16 * q, 0, 0);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) k[a][4 * q + j] = w[j];
+                    for (int j = 0; j < 4; ++j) w[a][4 * q + j] = x[j];
                 }
             }
+            const rsrc_t rs = make_rsrc(c.scales[0] + half[a].vec, half[a].n * 4);
+            scale[a] = __builtin_bit_cast(f32v4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * g, 0, 0));
         }
+    }
+};
+
+template <int D> struct KvValues {
+    static constexpr int VW = D == 256 ? 2 : 1, VB = D / 2;
+    uint32_t w[8][VW];
+    f32v4_t scale[2];
+
+    __device__ __forceinline__ void load(const KvPages& c, const KvHalf* half, int lane) {
+        const int l16 = lane & 15, g = lane >> 4;
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
             const rsrc_t rs = make_rsrc(c.scales[1] + half[a].vec, half[a].n * 4);
+            scale[a] = __builtin_bit_cast(f32v4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * g, 0, 0));
             const rsrc_t rv = make_rsrc(c.codes[1] + half[a].vec * VB, half[a].n * VB);
-            sv[a] = __builtin_bit_cast(f32v4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 16 * g, 0, 0));
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int off = (4 * g + r) * VB + l16 * (VB / 16);
+                const int off = 4 * g * VB + l16 * (VB / 16);
                 if constexpr (D == 64) {
-                    v[4 * a + r][0] = __builtin_amdgcn_raw_buffer_load_b16(rv, off, 0, 0);
+                    w[4 * a + r][0] = __builtin_amdgcn_raw_buffer_load_b16(rv, off + r * VB, 0, 0);
                 } else if constexpr (D == 128) {
-                    v[4 * a + r][0] = __builtin_amdgcn_raw_buffer_load_b32(rv, off, 0, 0);
+                    w[4 * a + r][0] = __builtin_amdgcn_raw_buffer_load_b32(rv, off + r * VB, 0, 0);
                 } else {
-                    const u32v2_t w = __builtin_amdgcn_raw_buffer_load_b64(rv, off, 0, 0);
-                    v[4 * a + r][0] = w[0], v[4 * a + r][1] = w[1];
+                    const u32v2_t x = __builtin_amdgcn_raw_buffer_load_b64(rv, off + r * VB, 0, 0);
+                    w[4 * a + r][0] = x[0], w[4 * a + r][1] = x[1];
                 }
             }
         }
@@ -156,57 +171,90 @@ __device__ __forceinline__ void nibble_columns(const uint32_t (&w)[8], f16x8_t (
     for (int n = 0; n < N; ++n) out[n] = __builtin_bit_cast(f16x8_t, f[n]);
 }
 
-// One column's query on the lane: its quarter of the vector (group g: elements
-// g D / 4 ...), scaled by a power of two to 2^14 .. 2^15 at the row's largest
-// element, as B operands of S^T = K Q^T for the operands of nibbles_a (odd
-// elements 1/16). PIECES = 2: x = hi + lo, 11 bits each. `zero` is the
-// accumulator's start, -8 sum x, that turns unsigned codes into signed ones;
-// `c` turns score * key scale into the exponent of 2.
-template <int D, int PIECES> struct KvQuery {
-    f16x8_t f[PIECES][D / 32];
-    float zero, c;
+// Queries as B operands of S^T = K Q^T for the operands of nibbles_a (odd
+// elements 1/16), made by the whole workgroup in LDS: the vector of a column is
+// scaled by a power of two to 2^14 .. 2^15 at its largest element; PIECES = 2:
+// x = hi + lo, 11 bits each. Eight elements are one lane's operand of one k-step:
+// lane group g = u / (D / 32) and step u % (D / 32) for elements 8 u and up.
+//   frag[piece][column tile][step][lane]
+//   zero[column]: the accumulator's start, -8 sum x, which turns the unsigned
+//                 codes into signed ones
+//   c[column]: turns score * key scale into the exponent of 2
+template <int D, int NC, int PIECES> struct KvQueries {
+    static constexpr int KW = D / 32;
+    f16x8_t frag[PIECES][NC][KW][64];
+};
 
-    template <typename T>
-    __device__ __forceinline__ void load(const T* q, bool live, float scale) {
-        float x[D / 4];
-        if (live) {
+// 16 threads a column, 16 NC columns by a workgroup of 256; row(col) gives the
+// column's vector or null. Both reductions run over the column's 16 lanes.
+__device__ __forceinline__ float lanes16_max(float v) {
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) load8(q + 8 * j, x + 8 * j);
-        } else {
+    for (int o = 1; o < 16; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+__device__ __forceinline__ float lanes16_sum(float v) {
 #pragma unroll
-            for (int j = 0; j < D / 4; ++j) x[j] = 0.f;
+    for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o);
+    return v;
+}
+template <int D, int NC, int PIECES, typename F>
+__device__ __forceinline__ void make_queries(KvQueries<D, NC, PIECES>& out, float* zero, float* cs, float scale, F row) {
+    constexpr int KW = D / 32, UNITS = D / 8, PER = (UNITS + 15) / 16;
+    const int part = threadIdx.x & 15;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+        const int col = threadIdx.x >> 4;
+        const auto* q = row(16 * n + col);
+        float x[PER][8];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            if (q && part + 16 * k < UNITS) {
+                load8(q + 8 * (part + 16 * k), x[k]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[k][i] = 0.f;
+            }
         }
         float m = 0.f;
 #pragma unroll
-        for (int j = 0; j < D / 4; ++j) m = fmaxf(m, fabsf(x[j]));
-        m = fmaxf(m, __shfl_xor(m, 16));
-        m = fmaxf(m, __shfl_xor(m, 32));
+        for (int k = 0; k < PER; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[k][i]));
+        m = lanes16_max(m);
         const bool some = m > 0.f && scale != 0.f;
         const int e = some ? 14 - ilogbf(m) : 0;
         const float sign = some ? copysignf(1.f, scale) : 0.f;
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
+        for (int k = 0; k < PER; ++k) {
+            const int u = part + 16 * k;
+            f16x8_t f[PIECES];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int el = nibble_slot(i);
-                float y = sign * ldexpf(x[8 * j + el], (el & 1) ? e - 4 : e);
+                float y = sign * ldexpf(x[k][el], (el & 1) ? e - 4 : e);
 #pragma unroll
                 for (int p = 0; p < PIECES; ++p) {
-                    const _Float16 h = (_Float16)y;
-                    f[p][j][i] = h;
-                    sum += (el & 1) ? 16.f * (float)h : (float)h;
-                    y -= (float)h;
+                    f[p][i] = (_Float16)y;
+                    const float r = (float)f[p][i];
+                    sum += (el & 1) ? 16.f * r : r;
+                    y -= r;
                 }
             }
+            if (u < UNITS) {
+#pragma unroll
+                for (int p = 0; p < PIECES; ++p) out.frag[p][n][u % KW][16 * (u / KW) + col] = f[p];
+            }
         }
-        sum += __shfl_xor(sum, 16);
-        sum += __shfl_xor(sum, 32);
-        zero = -8.f * 0x1p-24f * sum;
-        // finite and positive for any finite scale and query
-        c = some ? fminf(fmaxf(ldexpf(fabsf(scale) * 1.4426950408889634f, 24 - e), 0x1p-120f), 0x1p120f) : 1.f;
+        sum = lanes16_sum(sum);
+        if (part == 0) {
+            zero[16 * n + col] = -8.f * 0x1p-24f * sum;
+            // finite and positive for any finite scale and query
+            cs[16 * n + col] =
+                some ? fminf(fmaxf(ldexpf(fabsf(scale) * 1.4426950408889634f, 24 - e), 0x1p-120f), 0x1p120f) : 1.f;
+        }
     }
-};
+}
 
 // The keys a tile of columns walks over: the sinks' tiles, then the window's.
 struct KvWalk {
