@@ -21,11 +21,12 @@ namespace w4 {
 // known before the call.
 struct KvPlan {
     int column_tiles;  // of the sequence with the most rows
-    int nc;            // 16-column tiles a workgroup takes at once
+    bool prompt;       // kv_prompt_kernel, else kv_split_kernel
+    int nc;            // 16-column tiles of a wavefront
     int splits;        // parts of a sequence's keys
 };
 constexpr int kMaxSplits = 64;
-KvPlan kv_plan(const KvPages& c, int D, int group, int64_t max_rows, int64_t max_len, int64_t window,
+KvPlan kv_plan(const KvPages& c, int D, int group, int pieces, int64_t max_rows, int64_t max_len, int64_t window,
                int64_t sinks);
 
 // Partial results of a part: out[D] unnormalized, then the exponent's reference
@@ -34,18 +35,6 @@ __host__ __device__ constexpr int kv_partial_floats(int D) { return D + 4; }
 inline size_t kv_partial_bytes(int64_t vectors, int splits, int D) {
     return (size_t)vectors * splits * kv_partial_floats(D) * sizeof(float);
 }
-
-// The running softmax of one column on its four lanes. With x the score times
-// the key's scale (one fma with the reference mx) weights are 2^((x - mx) c):
-// exactly 1 at the reference, however large x c is. mx follows the maximum
-// lazily, once a weight would pass 2^kLift, so that most tiles scale nothing.
-constexpr float kLift = 4.f;
-// Weights times value scales enter the second product as 16-bit floats. Value
-// scales are taken relative to 2^e, e the exponent of the largest so far,
-// which is raised once a scale reaches 8 * 2^e; with 2^kBoost on top the operand
-// stays below 2^(kLift + 3 + kBoost) = 2^15, and what the format's least step
-// drops is 2^-33 of the largest value.
-constexpr int kBoost = 8;
 
 template <int D, int NC, int PIECES, typename TQ, typename TO>
 __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_kernel(KvPages c, KvAttn a, int column_tiles, int splits) {
@@ -126,16 +115,8 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
             qz[n] = q_zero[16 * n + l16];
             qc[n] = q_c[16 * n + l16];
         }
-        float mx[NC], thr[NC], l[NC];
-        f32v4_t o[NC][VW * VN];
-#pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            thr[n] = -INFINITY;  // nothing seen so far
-            mx[n] = l[n] = 0.f;
-#pragma unroll
-            for (int i = 0; i < VW * VN; ++i) o[n][i] = f32v4_t{0.f, 0.f, 0.f, 0.f};
-        }
-        float rv = 0.f, sv_max = 0.f;  // 2^(kBoost - e), 8 * 2^e
+        KvSoftmax<NC, PIECES, VW * VN> sm;
+        sm.start();
 
         for (; j < j1; j += 4) {
             const int t0 = walk.tile(j) * 32;
@@ -160,101 +141,15 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
             const bool whole = half[0].n == 16 && half[1].n == 16;
             const bool seen = whole && t0 + 31 <= p_lo &&
                               (a.window == 0 || t0 > max(p_hi, 0) - a.window || t0 + 31 < a.sinks);
-            float top[NC];
-            if (!seen) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int idx = 4 * g + r, t = t0 + 16 * h + idx;
-                        // a scale that no column sees may be stale: any bits
-                        const bool there = idx < half[h].n && t <= p_hi && (t > low_any || t < a.sinks);
-                        keys.scale[h][r] = there ? keys.scale[h][r] : 0.f;
-                        vals.scale[h][r] = there ? vals.scale[h][r] : 0.f;
-#pragma unroll
-                        for (int n = 0; n < NC; ++n) {
-                            const bool see = there && t <= pos[n] && (t > low[n] || t < a.sinks);
-                            z[n][h][r] = see ? fmaf(z[n][h][r], keys.scale[h][r], -mx[n]) : -INFINITY;
-                        }
-                    }
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-#pragma unroll
-                        for (int n = 0; n < NC; ++n) z[n][h][r] = fmaf(z[n][h][r], keys.scale[h][r], -mx[n]);
-            }
+            if (seen)
+                sm.scale(z, keys.scale);
+            else
+                sm.scale_masked(z, keys.scale, vals.scale, t0, g, half[0].n, half[1].n, p_hi, low_any, a.sinks, pos, low);
             locate(j + 4);
             keys.load(c, half, lane);
             entries(j + 8);
-            // references: rarely moved
-            bool move = false;
-#pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                top[n] = z[n][0][0];
-#pragma unroll
-                for (int i = 1; i < 8; ++i) top[n] = fmaxf(top[n], z[n][i >> 2][i & 3]);
-                move = move || top[n] > thr[n];
-            }
-            float big = vals.scale[0][0];
-#pragma unroll
-            for (int i = 1; i < 8; ++i) big = fmaxf(big, vals.scale[i >> 2][i & 3]);
-            if (__builtin_amdgcn_ballot_w64(move || big >= sv_max) != 0) {
-                float fv = 1.f;
-                big = wave_max(big);
-                if (big >= sv_max && big > 0.f) {
-                    const int e = min(max(ilogbf(big), -110), 110);
-                    const float r = ldexpf(1.f, kBoost - e);
-                    fv = rv > 0.f ? r / rv : 0.f;  // powers of two
-                    rv = r;
-                    sv_max = ldexpf(8.f, e);
-                }
-#pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                    float t = fmaxf(top[n], __shfl_xor(top[n], 16));
-                    t = fmaxf(t, __shfl_xor(t, 32));
-                    float f = 1.f;
-                    if (t > thr[n]) {  // alike on the column's four lanes
-                        const float to = mx[n] + t, by = to - mx[n];
-                        f = thr[n] > -INFINITY ? __builtin_amdgcn_exp2f(-by * qc[n]) : 0.f;
-                        mx[n] = to;
-                        thr[n] = kLift / qc[n];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) z[n][i >> 2][i & 3] -= by;
-                    }
-                    l[n] *= f;
-                    f *= fv;
-#pragma unroll
-                    for (int i = 0; i < VW * VN; ++i) o[n][i] *= f;
-                }
-            }
-            // weights, and their operands of the second product
-            f32v4_t sv[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) sv[h] = vals.scale[h] * rv;
             f16x8_t pf[NC][PIECES];
-#pragma unroll
-            for (int n = 0; n < NC; ++n) {
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    float y[2];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float p = __builtin_amdgcn_exp2f(z[n][(i + u) >> 2][(i + u) & 3] * qc[n]);
-                        l[n] += p;
-                        y[u] = p * sv[(i + u) >> 2][(i + u) & 3];
-                    }
-#pragma unroll
-                    for (int p = 0; p < PIECES; ++p) {
-                        const f16x2_t v = {(_Float16)y[0], (_Float16)y[1]};
-                        pf[n][p][i] = v[0];
-                        pf[n][p][i + 1] = v[1];
-                        y[0] -= (float)v[0];
-                        y[1] -= (float)v[1];
-                    }
-                }
-            }
+            sm.weights(z, vals.scale, qc, pf);
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
                 uint32_t words[8];
@@ -267,21 +162,20 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
 #pragma unroll
                     for (int n = 0; n < NC; ++n)
 #pragma unroll
-                        for (int p = 0; p < PIECES; ++p) o[n][w * VN + i] = mfma16(vf[i], pf[n][p], o[n][w * VN + i]);
+                        for (int p = 0; p < PIECES; ++p)
+                            sm.o[n][w * VN + i] = mfma16(vf[i], pf[n][p], sm.o[n][w * VN + i]);
             }
             vals.load(c, half, lane);
         }
 
         // the wavefronts' references and sums
+        sm.total();
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            l[n] += __shfl_xor(l[n], 16);
-            l[n] += __shfl_xor(l[n], 32);
+        for (int n = 0; n < NC; ++n)
             if (g == 0) {
-                stat[wave][16 * n + l16][0] = thr[n] > -INFINITY ? mx[n] * qc[n] : -INFINITY;
-                stat[wave][16 * n + l16][1] = l[n];
+                stat[wave][16 * n + l16][0] = sm.thr[n] > -INFINITY ? sm.mx[n] * qc[n] : -INFINITY;
+                stat[wave][16 * n + l16][1] = sm.l[n];
             }
-        }
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
@@ -294,13 +188,15 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
                 sum += mw > -INFINITY ? stat[w][16 * n + l16][1] * __builtin_amdgcn_exp2f(mw - top) : 0.f;
             }
             // this wavefront's share of the columns, d consecutive per lane
-            const float f = thr[n] > -INFINITY && rv > 0.f ? __builtin_amdgcn_exp2f(mx[n] * qc[n] - top) / rv : 0.f;
+            // (its own reference as stored: an fma of the product with -top would not give 0)
+            const float own = stat[wave][16 * n + l16][0];
+            const float f = own > -INFINITY && sm.rv > 0.f ? __builtin_amdgcn_exp2f(own - top) / sm.rv : 0.f;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int i = 0; i < VW * VN; i += 4)
                     *reinterpret_cast<f32v4_t*>(&lds.part[wave][l16][(4 * g + r) * (VW * VN) + i]) =
-                        f32v4_t{o[n][i][r], o[n][i + 1][r], o[n][i + 2][r], o[n][i + 3][r]} * f;
+                        f32v4_t{sm.o[n][i][r], sm.o[n][i + 1][r], sm.o[n][i + 2][r], sm.o[n][i + 3][r]} * f;
             __syncthreads();
             // 16 threads a column add the four and store
             const int cl = threadIdx.x >> 4, col = col0 + 16 * n + cl;
@@ -391,31 +287,20 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvPages c, KvAttn a, int s
 }
 
 // ---------------------------------------------------------------- host side
+template <int D, typename TO>
+hipError_t launch_kv_join(const KvPages& c, const KvAttn& a, int splits, hipStream_t st) {
+    hipLaunchKernelGGL((kv_join_kernel<D, TO>), dim3((unsigned)(((int64_t)c.rows * a.Hq + 3) / 4)), dim3(256), 0, st,
+                       c, a, splits);
+    return hipGetLastError();
+}
+
 template <int D, int NC, int PIECES, typename TQ, typename TO>
 hipError_t launch_kv_split_as(const KvPages& c, const KvAttn& a, const KvPlan& p, hipStream_t st) {
     const dim3 grid((unsigned)((int64_t)p.column_tiles * c.B), (unsigned)c.Hkv, (unsigned)p.splits);
     hipLaunchKernelGGL((kv_split_kernel<D, NC, PIECES, TQ, TO>), grid, dim3(256), 0, st, c, a, p.column_tiles,
                        p.splits);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
-    hipLaunchKernelGGL((kv_join_kernel<D, TO>), dim3((unsigned)(((int64_t)c.rows * a.Hq + 3) / 4)), dim3(256), 0, st,
-                       c, a, p.splits);
-    return hipGetLastError();
-}
-
-template <int D, int PIECES>
-hipError_t launch_kv_split(const KvPages& c, const KvAttn& a, bool q_bf16, bool out_bf16, hipStream_t st) {
-    const KvPlan p = kv_plan(c, D, a.group, a.max_rows, a.max_len, a.window, a.sinks);
-    auto go = [&](auto nc) -> hipError_t {
-        constexpr int NC = decltype(nc)::value;
-        if constexpr (PIECES == 1) return launch_kv_split_as<D, NC, 1, __bf16, __bf16>(c, a, p, st);
-        else if (!q_bf16 && !out_bf16) return launch_kv_split_as<D, NC, 2, float, float>(c, a, p, st);
-        else if (!q_bf16) return launch_kv_split_as<D, NC, 2, float, __bf16>(c, a, p, st);
-        else return launch_kv_split_as<D, NC, 2, __bf16, float>(c, a, p, st);
-    };
-    if constexpr (D < 256)
-        if (p.nc == 2) return go(std::integral_constant<int, 2>{});
-    return go(std::integral_constant<int, 1>{});
+    return e != hipSuccess || p.splits == 1 ? e : launch_kv_join<D, TO>(c, a, p.splits, st);
 }
 
 }  // namespace w4

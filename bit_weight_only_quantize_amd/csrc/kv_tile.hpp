@@ -138,13 +138,27 @@ template <int D> struct KvValues {
     }
 };
 
+// One nibble of each 16-bit half, as the code -8 .. 7 in a 16-bit float: bits 0-3
+// as 1024 + u less 1032, bits 4-7 (odd) as 1024 + 16 u times 1/16 less 72; exact.
+__device__ __forceinline__ uint32_t signed_pair(uint32_t x, bool odd) {
+    f16x2_t y;
+    if (odd) {
+        y = __builtin_bit_cast(f16x2_t, (x & 0x00F000F0u) | 0x64006400u);
+        y = __builtin_elementwise_fma(y, f16x2_t{(_Float16)0.0625f, (_Float16)0.0625f},
+                                      f16x2_t{(_Float16)-72.f, (_Float16)-72.f});
+    } else {
+        y = __builtin_bit_cast(f16x2_t, (x & 0x000F000Fu) | 0x64006400u);
+        y = y - f16x2_t{(_Float16)1032.f, (_Float16)1032.f};
+    }
+    return __builtin_bit_cast(uint32_t, y);
+}
+
 // The A operands of O^T = V^T P^T: operand n of word m holds, for the lane's
 // vector element 8 m + n (of its sixteenth), the 8 keys in k-slot order. The
 // words of two keys meet by halves, so that a 32-bit AND cuts both keys' nibble
-// of one element: 1024 + u as a 16-bit float, less 1032, and from bits 4-7
-// 1024 + 16 u, times 1/16 and less 72: the codes -8 .. 7, exact. (Unsigned ones
-// and a term -8 sum P would be cheaper, but where the heaviest keys' code is 0
-// the result is the difference of two large sums.)
+// of one element. Exact codes: unsigned subnormals and a term -8 sum P would be
+// cheaper, but where the heaviest keys' code is 0 the result is the difference of
+// two large sums.
 template <int N>
 __device__ __forceinline__ void nibble_columns(const uint32_t (&w)[8], f16x8_t (&out)[N]) {
     u32v4_t f[N];
@@ -155,16 +169,7 @@ __device__ __forceinline__ void nibble_columns(const uint32_t (&w)[8], f16x8_t (
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const uint32_t x = (n < 4 ? lo : hi) >> (n & 2 ? 8 : 0);
-            f16x2_t y;
-            if (n & 1) {
-                y = __builtin_bit_cast(f16x2_t, (x & 0x00F000F0u) | 0x64006400u);
-                y = __builtin_elementwise_fma(y, f16x2_t{(_Float16)0.0625f, (_Float16)0.0625f},
-                                              f16x2_t{(_Float16)-72.f, (_Float16)-72.f});
-            } else {
-                y = __builtin_bit_cast(f16x2_t, (x & 0x000F000Fu) | 0x64006400u);
-                y = y - f16x2_t{(_Float16)1032.f, (_Float16)1032.f};
-            }
-            f[n][i] = __builtin_bit_cast(uint32_t, y);
+            f[n][i] = signed_pair(x, n & 1);
         }
     }
 #pragma unroll
@@ -172,89 +177,260 @@ __device__ __forceinline__ void nibble_columns(const uint32_t (&w)[8], f16x8_t (
 }
 
 // Queries as B operands of S^T = K Q^T for the operands of nibbles_a (odd
-// elements 1/16), made by the whole workgroup in LDS: the vector of a column is
-// scaled by a power of two to 2^14 .. 2^15 at its largest element; PIECES = 2:
-// x = hi + lo, 11 bits each. Eight elements are one lane's operand of one k-step:
-// lane group g = u / (D / 32) and step u % (D / 32) for elements 8 u and up.
-//   frag[piece][column tile][step][lane]
-//   zero[column]: the accumulator's start, -8 sum x, which turns the unsigned
-//                 codes into signed ones
-//   c[column]: turns score * key scale into the exponent of 2
-template <int D, int NC, int PIECES> struct KvQueries {
-    static constexpr int KW = D / 32;
-    f16x8_t frag[PIECES][NC][KW][64];
+// elements 1/16). A column's vector is scaled by a power of two to 2^14 .. 2^15 at
+// its largest element; PIECES = 2: x = hi + lo, 11 bits each. Eight elements 8 u
+// and up are one lane's operand of one k-step: lane group g = u / (D / 32), step
+// u % (D / 32).
+//   zero: the accumulator's start, -8 sum x, which turns the unsigned codes into
+//         signed ones
+//   c:    turns score * key scale into the exponent of 2
+struct KvScaling {
+    int e;
+    float sign;
+    __device__ __forceinline__ KvScaling(float largest, float scale) {
+        const bool some = largest > 0.f && scale != 0.f;
+        e = some ? 14 - ilogbf(largest) : 0;
+        sign = some ? copysignf(1.f, scale) : 0.f;
+    }
+    static __device__ __forceinline__ float zero(float sum) { return -8.f * 0x1p-24f * sum; }
+    // finite and positive for any finite scale and query
+    __device__ __forceinline__ float c(float scale) const {
+        if (sign == 0.f) return 1.f;
+        return fminf(fmaxf(ldexpf(fabsf(scale) * 1.4426950408889634f, 24 - e), 0x1p-120f), 0x1p120f);
+    }
+    // one operand (and its share of sum x) from eight elements
+    template <int PIECES>
+    __device__ __forceinline__ float pieces(const float* x, f16x8_t (&f)[PIECES]) const {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int el = nibble_slot(i);
+            float y = sign * ldexpf(x[el], (el & 1) ? e - 4 : e);
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) {
+                f[p][i] = (_Float16)y;
+                const float r = (float)f[p][i];
+                sum += (el & 1) ? 16.f * r : r;
+                y -= r;
+            }
+        }
+        return sum;
+    }
 };
 
-// 16 threads a column, 16 NC columns by a workgroup of 256; row(col) gives the
-// column's vector or null. Both reductions run over the column's 16 lanes.
-__device__ __forceinline__ float lanes16_max(float v) {
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
-    return v;
-}
-__device__ __forceinline__ float lanes16_sum(float v) {
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o);
-    return v;
-}
+// By the whole workgroup in LDS: 16 threads a column, 16 NC columns by 256
+// threads; row(col) gives the column's vector or null.
+template <int D, int NC, int PIECES> struct KvQueries {
+    f16x8_t frag[PIECES][NC][D / 32][64];  // [..][k-step][lane]
+};
 template <int D, int NC, int PIECES, typename F>
 __device__ __forceinline__ void make_queries(KvQueries<D, NC, PIECES>& out, float* zero, float* cs, float scale, F row) {
     constexpr int KW = D / 32, UNITS = D / 8, PER = (UNITS + 15) / 16;
-    const int part = threadIdx.x & 15;
+    const int part = threadIdx.x & 15, col = threadIdx.x >> 4;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
-        const int col = threadIdx.x >> 4;
         const auto* q = row(16 * n + col);
-        float x[PER][8];
+        float x[PER][8], m = 0.f;
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-            if (q && part + 16 * k < UNITS) {
-                load8(q + 8 * (part + 16 * k), x[k]);
-            } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[k][i] = 0.f;
-            }
-        }
-        float m = 0.f;
-#pragma unroll
-        for (int k = 0; k < PER; ++k)
+            for (int i = 0; i < 8; ++i) x[k][i] = 0.f;
+            if (q && part + 16 * k < UNITS) load8(q + 8 * (part + 16 * k), x[k]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[k][i]));
-        m = lanes16_max(m);
-        const bool some = m > 0.f && scale != 0.f;
-        const int e = some ? 14 - ilogbf(m) : 0;
-        const float sign = some ? copysignf(1.f, scale) : 0.f;
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+        const KvScaling sc(m, scale);
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int u = part + 16 * k;
             f16x8_t f[PIECES];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int el = nibble_slot(i);
-                float y = sign * ldexpf(x[k][el], (el & 1) ? e - 4 : e);
-#pragma unroll
-                for (int p = 0; p < PIECES; ++p) {
-                    f[p][i] = (_Float16)y;
-                    const float r = (float)f[p][i];
-                    sum += (el & 1) ? 16.f * r : r;
-                    y -= r;
-                }
-            }
+            sum += sc.pieces<PIECES>(x[k], f);
             if (u < UNITS) {
 #pragma unroll
                 for (int p = 0; p < PIECES; ++p) out.frag[p][n][u % KW][16 * (u / KW) + col] = f[p];
             }
         }
-        sum = lanes16_sum(sum);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor(sum, o);
         if (part == 0) {
-            zero[16 * n + col] = -8.f * 0x1p-24f * sum;
-            // finite and positive for any finite scale and query
-            cs[16 * n + col] =
-                some ? fminf(fmaxf(ldexpf(fabsf(scale) * 1.4426950408889634f, 24 - e), 0x1p-120f), 0x1p120f) : 1.f;
+            zero[16 * n + col] = sc.zero(sum);
+            cs[16 * n + col] = sc.c(scale);
         }
     }
 }
+
+// By the wavefront in registers: a column's four lanes take a quarter each; q is
+// the column's vector or null.
+template <int D, int PIECES, typename T>
+__device__ __forceinline__ void load_query(const T* q, int g, float scale, f16x8_t (&frag)[PIECES][D / 32], float& zero,
+                                           float& c) {
+    float x[D / 4], m = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
+    if (q) {
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) load8(q + g * (D / 4) + 8 * w, x + 8 * w);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(x[i]));
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const KvScaling sc(m, scale);
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+        f16x8_t f[PIECES];
+        sum += sc.pieces<PIECES>(x + 8 * w, f);
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) frag[p][w] = f[p];
+    }
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    zero = sc.zero(sum);
+    c = sc.c(scale);
+}
+
+// ---------------------------------------------------------------- the running softmax
+// With x the score times the key's scale (one fma with the reference mx) weights
+// are 2^((x - mx) c): exactly 1 at the reference, however large x c is. mx
+// follows the maximum lazily, once a weight would pass 2^kLift, so that most
+// tiles scale nothing.
+constexpr float kLift = 4.f;
+// Weights times value scales enter the second product as 16-bit floats. Value
+// scales are taken relative to 2^e, e the exponent of the largest so far,
+// which is raised once a scale reaches 8 * 2^e; with 2^kBoost on top the operand
+// stays below 2^(kLift + 3 + kBoost) = 2^15, and what the format's least step
+// drops is 2^-33 of the largest value.
+constexpr int kBoost = 8;
+
+// One wavefront's NC column tiles; NO operands of 16 output elements each.
+template <int NC, int PIECES, int NO> struct KvSoftmax {
+    float mx[NC], thr[NC], l[NC];  // thr -inf: nothing seen so far; l: this lane's keys only
+    f32v4_t o[NC][NO];
+    float rv, sv_max;  // 2^(kBoost - e), 8 * 2^e
+
+    __device__ __forceinline__ void start() {
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            thr[n] = -INFINITY;
+            mx[n] = l[n] = 0.f;
+#pragma unroll
+            for (int i = 0; i < NO; ++i) o[n][i] = f32v4_t{0.f, 0.f, 0.f, 0.f};
+        }
+        rv = sv_max = 0.f;
+    }
+
+    // z: scores in, relative to mx out
+    __device__ __forceinline__ void scale(f32v4_t (&z)[NC][2], const f32v4_t (&ks)[2]) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int n = 0; n < NC; ++n) z[n][h][r] = fmaf(z[n][h][r], ks[h][r], -mx[n]);
+    }
+    // The same where rows end or pages are missing: keys t0 .. t0 + 31, of which n0 and n1
+    // of the halves are there, columns at pos that see t <= pos and t > low or t < sinks.
+    // Scales of keys that no column sees may be stale, any bits: they become 0.
+    __device__ __forceinline__ void scale_masked(f32v4_t (&z)[NC][2], f32v4_t (&ks)[2], f32v4_t (&vs)[2], int t0, int g,
+                                                 int n0, int n1, int p_hi, int low_any, int sinks,
+                                                 const int (&pos)[NC], const int (&low)[NC]) const {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int idx = 4 * g + r, t = t0 + 16 * h + idx;
+                const bool there = idx < (h ? n1 : n0) && t <= p_hi && (t > low_any || t < sinks);
+                ks[h][r] = there ? ks[h][r] : 0.f;
+                vs[h][r] = there ? vs[h][r] : 0.f;
+#pragma unroll
+                for (int n = 0; n < NC; ++n) {
+                    const bool see = there && t <= pos[n] && (t > low[n] || t < sinks);
+                    z[n][h][r] = see ? fmaf(z[n][h][r], ks[h][r], -mx[n]) : -INFINITY;
+                }
+                __builtin_amdgcn_sched_barrier(0);  // few masks at a time: scalar registers
+            }
+    }
+
+    // Weights of a tile, as operands of the second product.
+    __device__ __forceinline__ void weights(f32v4_t (&z)[NC][2], const f32v4_t (&vs)[2], const float (&c)[NC],
+                                            f16x8_t (&pf)[NC][PIECES]) {
+        float top[NC];
+        bool move = false;
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            top[n] = z[n][0][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) top[n] = fmaxf(top[n], z[n][i >> 2][i & 3]);
+            move = move || top[n] > thr[n];
+        }
+        float big = vs[0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) big = fmaxf(big, vs[i >> 2][i & 3]);
+        if (__builtin_amdgcn_ballot_w64(move || big >= sv_max) != 0) {  // rarely
+            float fv = 1.f;
+            big = wave_max(big);
+            if (big >= sv_max && big > 0.f) {
+                const int e = min(max(ilogbf(big), -110), 110);
+                const float r = ldexpf(1.f, kBoost - e);
+                fv = rv > 0.f ? r / rv : 0.f;  // powers of two
+                rv = r;
+                sv_max = ldexpf(8.f, e);
+            }
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+                float t = fmaxf(top[n], __shfl_xor(top[n], 16));
+                t = fmaxf(t, __shfl_xor(t, 32));
+                float f = 1.f;
+                if (t > thr[n]) {  // alike on the column's four lanes
+                    const float to = mx[n] + t, by = to - mx[n];
+                    f = thr[n] > -INFINITY ? __builtin_amdgcn_exp2f(-by * c[n]) : 0.f;
+                    mx[n] = to;
+                    thr[n] = kLift / c[n];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) z[n][i >> 2][i & 3] -= by;
+                }
+                l[n] *= f;
+                f *= fv;
+#pragma unroll
+                for (int i = 0; i < NO; ++i) o[n][i] *= f;
+            }
+        }
+        const f32v4_t sv[2] = {vs[0] * rv, vs[1] * rv};
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                float y[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float p = __builtin_amdgcn_exp2f(z[n][(i + u) >> 2][(i + u) & 3] * c[n]);
+                    l[n] += p;
+                    y[u] = p * sv[(i + u) >> 2][(i + u) & 3];
+                }
+#pragma unroll
+                for (int p = 0; p < PIECES; ++p) {
+                    const f16x2_t v = {(_Float16)y[0], (_Float16)y[1]};  // to nearest
+                    pf[n][p][i] = v[0];
+                    pf[n][p][i + 1] = v[1];
+                    y[0] -= (float)v[0];
+                    y[1] -= (float)v[1];
+                }
+            }
+    }
+
+    // the whole sum of a column, on its four lanes
+    __device__ __forceinline__ void total() {
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            l[n] += __shfl_xor(l[n], 16);
+            l[n] += __shfl_xor(l[n], 32);
+        }
+    }
+};
 
 // The keys a tile of columns walks over: the sinks' tiles, then the window's.
 struct KvWalk {

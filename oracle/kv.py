@@ -125,15 +125,17 @@ def kv_attention(q, k, v, scale, window=0, sinks=0):
             t = t[(t > p - window) | (t < sinks)]
         if t.size == 0:
             continue
-        for h in range(Hq):
-            K, V, x = k[g[h]][t], v[g[h]][t], q[i, h]
-            z = scale * (K @ x)
-            m = z.max()
+        for j in range(k.shape[0]):
+            K, V, h = k[j][t], v[j][t], g == j                 # its query heads together
+            x = q[i, h]                                        # [heads][D]
+            z = scale * (x @ K.T)                              # [heads][t]
+            m = z.max(axis=1, keepdims=True)
             e = np.exp(z - m)
-            out[i, h] = e @ V / e.sum()
-            A[i, h] = e @ np.abs(V) / e.sum()
-            lse[i, h] = m + np.log(e.sum())
+            total = e.sum(axis=1, keepdims=True)
+            out[i, h] = e @ V / total
+            A[i, h] = e @ np.abs(V) / total
+            lse[i, h] = (m + np.log(total))[:, 0]
             K8 = np.abs(K) + 8 / 7 * np.abs(K).max(axis=1, keepdims=True)
-            Z[i, h] = (abs(scale) * (K8 @ np.abs(x))).max()
-            Zmax[i, h] = (abs(scale) * K8.sum(1) * np.abs(x).max()).max()
+            Z[i, h] = abs(scale) * (np.abs(x) @ K8.T).max(axis=1)
+            Zmax[i, h] = abs(scale) * K8.sum(axis=1).max() * np.abs(x).max(axis=1)
     return out, lse, A, Z, Zmax

@@ -424,3 +424,65 @@ def test_positions_past_2_to_31_bytes():
     ref = oracle.kv_attention(q, deq[None], deq[None], float(np.float32(128 ** -0.5)))
     e, el = bounds(ref, 128, 40, np.abs(deq).max(), "f32", "f32")
     assert (np.abs(got.cpu().numpy() - ref[0]) <= e).all() and (np.abs(lse.cpu().numpy() - ref[1]) <= el).all()
+
+
+# Many columns a kv head over hundreds of keys or more: sizes at which the estimate picks the kernel
+# that shares unpacked keys between wavefronts (and, with few of them, splits their keys as well).
+def _large(lens, rows, Hkv, G, D, page, q_dtype, out_dtype, window=0, sinks=0, bad=()):
+    name = f"large.{D}.{lens}.{rows}"
+    s = Batch(lens, rows, Hkv, D, page, name)
+    Hq = Hkv * G
+    q = values((s.rows, Hq, D), name + ".q", q_dtype, seed=2)
+    cache, b = s.cache(), s.batch(max_rows=max(rows), max_len=max(lens))
+    table = None if s.table is None else s.table.copy()
+    for seq, j in bad:
+        table[seq, j] = -1
+    if bad:
+        b.table.copy_(torch.from_numpy(table))
+    out = torch.full((s.rows + 3, Hq, D), 9.0, dtype=DT[out_dtype], device="cuda")
+    qd = torch.cat([to_dev(q, q_dtype), torch.full((3, Hq, D), float("nan"), dtype=DT[q_dtype], device="cuda")])
+    got, lse = w4.kv_attention(qd, cache, b, window=window, sinks=sinks, out=out, want_lse=True)
+    again = w4.kv_attention(qd, cache, b, window=window, sinks=sinks)
+    assert torch.equal(again[:s.rows].to(got.dtype), got[:s.rows]) or q_dtype != out_dtype
+    assert (got[s.rows:] == 9.0).all(), "rows of no sequence written"
+    scale = float(np.float32(D ** -0.5))
+    pick, refs = [], []
+    for seq in range(s.B):                                     # some rows of each: the ends, tile edges, others
+        n = s.n[seq]
+        for i in sorted({0, 1, n // 3, n // 2, n - 2, n - 1} & set(range(n))):
+            p = s.lens[seq] - n + i
+            t = np.arange(p + 1)
+            if bad:
+                t = t[(table[seq, t // page] >= 0)]
+            if window:
+                t = t[(t > p - window) | (t < sinks)]
+            pick.append(s.first[seq] + i)
+            refs.append(oracle.kv_attention(q[pick[-1]][None], s.deq[0][seq][:, t], s.deq[1][seq][:, t], scale))
+    check(s, got[pick], lse[pick], [np.concatenate(r) for r in zip(*refs)], q_dtype, out_dtype)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (333, 5), (64, 40)])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 0), (128, 32), (256, 16)])
+def test_attention_large_prompts_bf16(D, page, window, sinks):
+    _large([628, 530, 700, 611], [128, 101, 120, 77], 2, 64, D, page, "bf16", "bf16", window, sinks)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_large_prompts_fp32(D):
+    _large([3628, 3530, 3700, 3611], [128, 128, 120, 127], 2, 64, D, 64, "f32", "f32")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_large_prompts_in_parts(D):
+    _large([9001], [130], 1, 64, D, 64, "bf16", "bf16")
+    _large([30001], [130], 1, 64, D, 0, "bf16", "f32")
+
+
+def test_attention_large_prompts_missing_pages():
+    _large([628, 530, 700, 611], [128, 101, 120, 77], 2, 64, 128, 16, "bf16", "bf16",
+           bad=[(0, 0), (0, 39), (1, 7), (1, 8), (2, 43), (3, 1)])
+
+
+def test_attention_large_prompt_without_a_context():
+    """Rows from the first position on: every tile is cut by the causal edge somewhere."""
+    _large([700, 611, 640, 655], [700, 611, 640, 655], 2, 32, 128, 16, "bf16", "bf16")
