@@ -69,6 +69,35 @@ def test_write_equals_the_single_sequence_codec():
         assert torch.equal(c[0], codes) and torch.equal(s[0].view(torch.int32), scales.view(torch.int32))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_write_values_at_the_borders_between_codes(dtype):
+    """Values on, next to and between the borders (k + 0.5) s, for scales over the whole range of the type
+    down to its subnormals: the codes of the correctly rounded quotient, bit for bit."""
+    rng = np.random.default_rng(5)
+    L, Hkv, D = 512, 4, 128
+    m = np.exp2(rng.uniform(-148, 127, (L, Hkv, 1))).astype(np.float32)
+    m[::4] = np.exp2(rng.uniform(-3, 3, m[::4].shape)).astype(np.float32)
+    if dtype == "bf16":
+        m = (m.view(np.uint32) & np.uint32(0xFFFF0000)).view(np.float32)
+    m = np.maximum(m, np.float32(2.0 ** -133))
+    s = (m / np.float32(7.5)).astype(np.float64)
+    k = rng.integers(0, 8, (L, Hkv, D))
+    x = np.minimum(((k + 0.5) * s).astype(np.float32), m)
+    x[..., 1::3] = (((2 * k + 1) / 15)[..., 1::3] * m).astype(np.float32)
+    bits = x.view(np.int32) + (0 if dtype == "bf16" else rng.integers(-2, 3, x.shape).astype(np.int32))
+    x = np.clip(np.maximum(bits, 0).view(np.float32), 0, m)
+    if dtype == "bf16":
+        x = ((x.view(np.uint32) + np.uint32(0x8000)) & np.uint32(0xFFFF0000)).view(np.float32)
+        x = np.minimum(x, m)
+    x[..., 0] = m[..., 0]
+    x = np.ascontiguousarray(np.where(rng.random(x.shape) < 0.5, x, -x), dtype=np.float32)
+    cache = w4.kv_pages(1, Hkv, L, D)
+    w4.kv_write(to_dev(x, dtype), None, cache, w4.KVBatch(torch.tensor([L], dtype=torch.int32, device="cuda"), rows=L))
+    c, sc = oracle.kv_quantize(np.ascontiguousarray(x.transpose(1, 0, 2)))
+    assert np.array_equal(cache.k_scales[0].cpu().numpy().view(np.uint32), sc.view(np.uint32))
+    assert np.array_equal(cache.k_codes[0].cpu().numpy(), c)
+
+
 def test_write_one_half_and_mixed_types():
     s = Batch([40, 9], [7, 2], 2, 64, 16, "half")
     cache = s.cache(upto=[33, 7])
