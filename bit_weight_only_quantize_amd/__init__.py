@@ -489,7 +489,7 @@ class KVPages:
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.num_pages, self.Hkv, self.page_size = k_scales.shape
         self.D = 2 * k_codes.shape[3]
-        self.device = k_codes.device
+        self.device, self.index = k_codes.device, k_codes.get_device()
         self._c = _W4KvPages(self.D, self.num_pages, self.Hkv, self.page_size, _ptr(k_codes), _ptr(k_scales),
                              _ptr(v_codes), _ptr(v_scales))
         self._ref = ctypes.byref(self._c)
@@ -535,7 +535,8 @@ class KVBatch:
         if table is not None and table.shape[0] != B:
             raise ValueError(f"table must hold {B} sequences")
         self.lens, self.table, self.starts = lens, table, starts
-        self.B, self.rows, self.device = B, B if rows is None else int(rows), lens.device
+        self.B, self.rows = B, B if rows is None else int(rows)
+        self.device, self.index = lens.device, lens.get_device()
         width = table.shape[1] if table is not None else 0
         stride = table.stride(0) if table is not None and B > 1 else width
         self._c = _W4KvBatch(B, self.rows, int(max_rows or 0), int(max_len or 0), _ptr(lens), _ptr(starts),
@@ -545,29 +546,30 @@ class KVBatch:
 
 def _rows_desc(t: torch.Tensor, name: str, cache: KVPages, batch: KVBatch, heads: int) -> _W4Rows:
     """w4_rows of a tensor [rows or more][heads][D]."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != cache.D or t.shape[0] < batch.rows:
-        raise ValueError(f"{name} must be [{batch.rows} or more][{heads}][{cache.D}], not {tuple(t.shape)}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != cache.D or shape[0] < batch.rows:
+        raise ValueError(f"{name} must be [{batch.rows} or more][{heads}][{cache.D}], not {tuple(shape)}")
     code = _ROW_TYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be float32 or bfloat16")
-    rs, hs, one = t.stride()
-    if one != 1:
+    if strides[2] != 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
-    if t.device != cache.device:
+    if t.get_device() != cache.index:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
-    return _W4Rows(t.data_ptr(), code, rs, hs)
+    return _W4Rows(t.data_ptr(), code, strides[0], strides[1])
 
 
 def _kv_call(cache: KVPages, batch: KVBatch, f, *args) -> None:
-    """f(*args, stream) on the cache's device."""
-    if batch.device != cache.device:
+    """f(*args, stream) on the cache's device and its current stream."""
+    if batch.index != cache.index:
         raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
-    if torch.cuda.current_device() == cache.device.index:
-        rc = f(*args, _stream(cache.device))
+    if torch.cuda.current_device() == cache.index:
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(cache.index))
     else:
-        with torch.cuda.device(cache.device):
-            rc = f(*args, _stream(cache.device))
-    _check(rc)
+        with torch.cuda.device(cache.index):
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(cache.index))
+    if rc:
+        _check(rc)
 
 
 def kv_write(k: Optional[torch.Tensor], v: Optional[torch.Tensor], cache: KVPages, batch: KVBatch) -> None:
@@ -590,10 +592,10 @@ def kv_read(cache: KVPages, batch: KVBatch, dtype: torch.dtype = torch.bfloat16,
 
 
 def kv_attention_workspace(cache: KVPages, batch: KVBatch, Hq: int, window: int = 0,
-                           sinks: int = 0) -> Optional[torch.Tensor]:
-    """A workspace for kv_attention with these sizes (None where it needs none)."""
+                           sinks: int = 0) -> torch.Tensor:
+    """A workspace for kv_attention with these sizes (empty where it needs none)."""
     n = int(lib().w4_kv_attention_workspace_bytes(cache._ref, batch._ref, Hq, window, sinks))
-    return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
 def kv_attention(q: torch.Tensor, cache: KVPages, batch: KVBatch, scale: Optional[float] = None,
@@ -604,26 +606,30 @@ def kv_attention(q: torch.Tensor, cache: KVPages, batch: KVBatch, scale: Optiona
     cached positions, with window > 0 over the last `window` and the first `sinks` ones only. scale:
     1 / sqrt(D) by default. Returns out (q's type unless given), or (out, lse) with lse fp32 [rows][Hq]
     when lse is given or want_lse. Rows of no sequence are left as they are; a row that sees nothing gets
-    0 and -inf."""
+    0 and -inf. workspace: kv_attention_workspace(...)'s (allocated for the call by default); calls that
+    may overlap need their own."""
     Hq = q.shape[1] if q.dim() == 3 else 0
     dq = _rows_desc(q, "q", cache, batch, Hq)
     if out is None:
         out = torch.empty((q.shape[0], Hq, cache.D), dtype=q.dtype, device=q.device)
     do = _rows_desc(out, "out", cache, batch, Hq)
-    if lse is None and want_lse:
-        lse = torch.empty((q.shape[0], Hq), dtype=torch.float32, device=q.device)
+    plse = None
     if lse is not None:
         _dev(lse, "lse")
         if lse.dtype != torch.float32 or lse.dim() != 2 or lse.shape[0] < batch.rows or lse.shape[1] != Hq \
-                or lse.device != cache.device:
+                or lse.get_device() != cache.index:
             raise ValueError(f"lse must be float32 [{batch.rows} or more][{Hq}] on the cache's device")
+        plse = lse.data_ptr()
+    elif want_lse:
+        lse = out.new_empty((q.shape[0], Hq), dtype=torch.float32)
+        plse = lse.data_ptr()
     if workspace is None:
         workspace = kv_attention_workspace(cache, batch, Hq, window, sinks)
-    elif workspace.device != cache.device or not workspace.is_contiguous():
+    elif workspace.get_device() != cache.index or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the cache's device")
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _kv_call(cache, batch, lib().w4_kv_attention, cache._ref, batch._ref, dq, Hq,
-             cache.D ** -0.5 if scale is None else scale, window, sinks, do, _ptr(lse), _ptr(workspace), nbytes)
+             cache.D ** -0.5 if scale is None else scale, window, sinks, do, plse, workspace.data_ptr() or None,
+             workspace.nbytes)
     return out if lse is None else (out, lse)
 
 
