@@ -24,6 +24,7 @@ import torch
 __all__ = [
     "SCHEME_IDS", "W4Error", "QuantizedMatrix", "lib", "lib_path", "packed_sizes", "quantize_pack",
     "empty_quantized", "gemv", "gemv_into", "gemv_multi", "gemv_multi_into", "gemm", "moe_route", "moe_workspace_bytes", "moe_gemv",
+    "KVPages", "KVBatch", "kv_pages", "kv_write", "kv_read", "kv_attention", "kv_attention_workspace",
 ]
 
 SCHEME_IDS = {"sym4_g128": 0, "aff4_g64": 1, "aff8_g64": 2}

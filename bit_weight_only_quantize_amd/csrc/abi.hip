@@ -771,7 +771,8 @@ static int kv_check_pages(const w4_kv_pages* c, const w4_kv_batch* b, w4::KvPage
     if (c->D != 64 && c->D != 128 && c->D != 256)
         return fail(W4_ESHAPE, "D=%d: head vectors of 64, 128 or 256 values", (int)c->D);
     if (c->Hkv < 1 || c->num_pages < 1 || c->page_size < 1 || c->num_pages > kInt31 ||
-        c->page_size > kInt31 || c->Hkv > 65535)
+        c->page_size > kInt31 || c->Hkv > 65535 ||
+        c->num_pages * c->Hkv > (1LL << 47) / c->page_size)  // head vectors: byte offsets fit 63 bits
         return fail(W4_ESHAPE, "num_pages=%lld Hkv=%lld page_size=%lld out of range",
                     (long long)c->num_pages, (long long)c->Hkv, (long long)c->page_size);
     if (b->B < 0 || b->rows < 0 || b->max_rows < 0 || b->max_len < 0 || b->B > (1 << 20) ||
@@ -805,6 +806,8 @@ static int kv_check_pages(const w4_kv_pages* c, const w4_kv_batch* b, w4::KvPage
         return fail(W4_ESHAPE, "%lld pages for %lld sequences without a table",
                     (long long)c->num_pages, (long long)b->B);
     }
+    if (cap > kInt31 - 64)  // a tile of keys behind the last one still has a 31-bit position
+        return fail(W4_ESHAPE, "capacity=%lld positions of a sequence out of range", (long long)cap);
     v->codes[0] = c->k_codes;
     v->codes[1] = c->v_codes;
     v->scales[0] = c->k_scales;
@@ -830,6 +833,8 @@ static int64_t kv_max_rows(const w4_kv_batch* b) {
     if (!b->starts) return b->rows / b->B;
     return b->max_rows > 0 && b->max_rows < b->rows ? b->max_rows : b->rows;
 }
+// Windows and sinks past any position are alike.
+static int64_t kv_positions(int64_t v) { return v < kInt31 ? v : kInt31; }
 static int64_t kv_max_len(const w4_kv_batch* b, const w4::KvPages& v) {
     return b->max_len > 0 && b->max_len < v.capacity ? b->max_len : v.capacity;
 }
@@ -916,7 +921,7 @@ size_t w4_kv_attention_workspace_bytes(const w4_kv_pages* cache, const w4_kv_bat
         kv_check_heads(cache, batch, Hq, window, sinks))
         return 0;
     return w4::kv_attention_workspace(v, cache->D, Hq, kv_max_rows(batch), kv_max_len(batch, v),
-                                      window, sinks);
+                                      kv_positions(window), kv_positions(sinks));
 }
 
 int w4_kv_attention(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows* q,
@@ -929,6 +934,8 @@ int w4_kv_attention(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4
     if (rc) return rc;
     if (!isfinite(scale)) return fail(W4_EINVAL, "scale is not finite");
     if (batch->B == 0 || batch->rows == 0) return ok();
+    window = kv_positions(window);
+    sinks = kv_positions(sinks);
     if (!q || !out) return fail(W4_EINVAL, "null q or out");
     rc = kv_check_rows(q, "q", batch->rows, Hq, cache->D, false);
     if (rc) return rc;
@@ -952,8 +959,8 @@ int w4_kv_attention(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4
     a.out_head = out->head_stride;
     a.Hq = (int)Hq;
     a.group = (int)(Hq / cache->Hkv);
-    a.window = (int)(window < kInt31 ? window : kInt31);
-    a.sinks = (int)(sinks < kInt31 ? sinks : kInt31);
+    a.window = (int)window;
+    a.sinks = (int)sinks;
     a.max_rows = (int)max_rows;
     a.max_len = (int)max_len;
     a.scale = scale;

@@ -40,6 +40,9 @@ template <int D, int NC, int PIECES, typename TQ, typename TO>
 __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_kernel(KvPages c, KvAttn a, int column_tiles, int splits) {
     constexpr int KW = D / 32, VN = D == 64 ? 4 : 8, VW = KvValues<D>::VW;
     constexpr int LD = D + 4;  // floats a column in LDS
+    // exact key codes where results are fp32; for bf16 ones they would cost 14% of a long
+    // context's time (53 -> 60 us, two sequences of 131072 positions)
+    constexpr bool EXACT = PIECES == 2;
     constexpr bool HOLD = PIECES * KW * NC <= 4;  // queries in registers, else read from LDS for every tile
     union Lds {
         KvQueries<D, NC, PIECES> q;
@@ -89,7 +92,7 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
         vals.load(c, half, lane);
         entries(j + 4);
 
-        make_queries<D, NC, PIECES>(lds.q, q_zero, q_c, a.scale, [&](int i) -> const TQ* {
+        make_queries<EXACT, D, NC, PIECES>(lds.q, q_zero, q_c, a.scale, [&](int i) -> const TQ* {
             const int col = col0 + i, row = col / a.group;
             return col < columns ? static_cast<const TQ*>(a.q) + (int64_t)(s.first + row) * a.q_row +
                                        (int64_t)(head * a.group + col - row * a.group) * a.q_head
@@ -130,7 +133,7 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int w = 0; w < KW; ++w) {
-                    const f16x8_t k = nibbles_a(keys.w[h][w]);
+                    const f16x8_t k = nibbles_a<EXACT>(keys.w[h][w]);
 #pragma unroll
                     for (int n = 0; n < NC; ++n)
 #pragma unroll

@@ -94,7 +94,7 @@ template <int D> struct KvBring {
             for (int h = 0; h < HALVES; ++h) {
                 const int a = HALVES == 2 ? h : s;
 #pragma unroll
-                for (int j = 0; j < KW; ++j) st.k[tile][a][j][lane] = nibbles_a(raw[h * KW + j]);
+                for (int j = 0; j < KW; ++j) st.k[tile][a][j][lane] = nibbles_a<true>(raw[h * KW + j]);
                 if (lane == 0) st.n[tile][a] = n[h];
             }
             const int l16 = lane & 15, g = lane >> 4;
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(512, 2) void kv_prompt_kernel(KvPages c, KvAttn a, 
         const int p_hi = any ? pos0 + min(w0 + CW - 1, columns - 1) / a.group : -1;
         const int low_any = a.window > 0 ? max(p_lo, 0) - a.window : -1;
         f16x8_t q[NC][PIECES][KW];
-        float qz[NC], qc[NC];
+        float qc[NC];
         int pos[NC], low[NC];
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
@@ -172,7 +172,7 @@ __global__ __launch_bounds__(512, 2) void kv_prompt_kernel(KvPages c, KvAttn a, 
             const TQ* p = live ? static_cast<const TQ*>(a.q) + (int64_t)(s.first + row) * a.q_row +
                                      (int64_t)(head * a.group + col - row * a.group) * a.q_head
                                : nullptr;
-            load_query<D, PIECES>(p, g, a.scale, q[n], qz[n], qc[n]);
+            load_query<D, PIECES>(p, g, a.scale, q[n], qc[n]);
             pos[n] = live ? pos0 + row : -1;
             low[n] = a.window > 0 ? max(pos[n], 0) - a.window : -1;
         }
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(512, 2) void kv_prompt_kernel(KvPages c, KvAttn a, 
                 __builtin_amdgcn_s_setprio(1);  // products before the other wavefront's softmax
                 f32v4_t z[NC][2];
 #pragma unroll
-                for (int n = 0; n < NC; ++n) z[n][0] = z[n][1] = f32v4_t{qz[n], qz[n], qz[n], qz[n]};
+                for (int n = 0; n < NC; ++n) z[n][0] = z[n][1] = f32v4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int w = 0; w < KW; ++w)
 #pragma unroll

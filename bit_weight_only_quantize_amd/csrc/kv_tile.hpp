@@ -11,11 +11,12 @@
 // P^T, wants of P on that lane: the weights go from one product to the next
 // in registers.
 //
-// Codes to 16-bit floats: a nibble u in bits 0-3 of a 16-bit half is the
-// subnormal u * 2^-24, in bits 4-7 it is u * 2^-20, and the matrix cores take
-// subnormals as they are, so one AND makes two operands. The factors are powers
-// of two and go into the other operand or the result; the offset of 8 is a
-// term that does not depend on the code.
+// Codes to 16-bit floats: exact codes -8 .. 7 in two instructions a pair
+// (signed_pair). Or, for the keys under bf16 queries, in one: a nibble u in bits
+// 0-3 of a 16-bit half is the subnormal u * 2^-24, in bits 4-7 it is u * 2^-20, and
+// the matrix cores take subnormals as they are. The factors are powers of two and
+// go into the other operand or the result; the offset of 8 is a term that does not
+// depend on the code.
 #pragma once
 
 #include "kv_attention.hpp"
@@ -33,12 +34,35 @@ __device__ __forceinline__ f32v4_t mfma16(const f16x8_t a, const f16x8_t b, cons
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// The word's eight nibbles as one A operand, unsigned subnormals; slot order
-// (elements) 0 4 1 5 2 6 3 7, the odd elements 16 times the even ones' factor.
-__device__ __forceinline__ f16x8_t nibbles_a(uint32_t w) {
+// One nibble of each 16-bit half, as the code -8 .. 7 in a 16-bit float: bits 0-3
+// as 1024 + u less 1032, bits 4-7 (odd) as 1024 + 16 u times 1/16 less 72; exact.
+__device__ __forceinline__ uint32_t signed_pair(uint32_t x, bool odd) {
+    f16x2_t y;
+    if (odd) {
+        y = __builtin_bit_cast(f16x2_t, (x & 0x00F000F0u) | 0x64006400u);
+        y = __builtin_elementwise_fma(y, f16x2_t{(_Float16)0.0625f, (_Float16)0.0625f},
+                                      f16x2_t{(_Float16)-72.f, (_Float16)-72.f});
+    } else {
+        y = __builtin_bit_cast(f16x2_t, (x & 0x000F000Fu) | 0x64006400u);
+        y = y - f16x2_t{(_Float16)1032.f, (_Float16)1032.f};
+    }
+    return __builtin_bit_cast(uint32_t, y);
+}
+
+// The word's eight nibbles as one A operand of the scores; slot order (elements)
+// 0 4 1 5 2 6 3 7. EXACT: codes -8 .. 7. Otherwise unsigned subnormals, the odd
+// elements 16 times the even ones' factor: half the instructions, but scores are then
+// the difference of sum q u and 8 sum q and lose three bits in it (fp32 results
+// were 2 to 7e-6 off in norm, 3 to 8e-7 with exact codes; bf16 ones do not show it).
+template <bool EXACT> __device__ __forceinline__ f16x8_t nibbles_a(uint32_t w) {
     const uint32_t h = w >> 8;
-    const u32v4_t f = {w & 0x000F000Fu, w & 0x00F000F0u, h & 0x000F000Fu, h & 0x00F000F0u};
-    return __builtin_bit_cast(f16x8_t, f);
+    if constexpr (EXACT) {
+        const u32v4_t f = {signed_pair(w, false), signed_pair(w, true), signed_pair(h, false), signed_pair(h, true)};
+        return __builtin_bit_cast(f16x8_t, f);
+    } else {
+        const u32v4_t f = {w & 0x000F000Fu, w & 0x00F000F0u, h & 0x000F000Fu, h & 0x00F000F0u};
+        return __builtin_bit_cast(f16x8_t, f);
+    }
 }
 __device__ constexpr int nibble_slot(int i) { return (i >> 1) + 4 * (i & 1); }  // slot -> element
 
@@ -138,21 +162,6 @@ template <int D> struct KvValues {
     }
 };
 
-// One nibble of each 16-bit half, as the code -8 .. 7 in a 16-bit float: bits 0-3
-// as 1024 + u less 1032, bits 4-7 (odd) as 1024 + 16 u times 1/16 less 72; exact.
-__device__ __forceinline__ uint32_t signed_pair(uint32_t x, bool odd) {
-    f16x2_t y;
-    if (odd) {
-        y = __builtin_bit_cast(f16x2_t, (x & 0x00F000F0u) | 0x64006400u);
-        y = __builtin_elementwise_fma(y, f16x2_t{(_Float16)0.0625f, (_Float16)0.0625f},
-                                      f16x2_t{(_Float16)-72.f, (_Float16)-72.f});
-    } else {
-        y = __builtin_bit_cast(f16x2_t, (x & 0x000F000Fu) | 0x64006400u);
-        y = y - f16x2_t{(_Float16)1032.f, (_Float16)1032.f};
-    }
-    return __builtin_bit_cast(uint32_t, y);
-}
-
 // The A operands of O^T = V^T P^T: operand n of word m holds, for the lane's
 // vector element 8 m + n (of its sixteenth), the 8 keys in k-slot order. The
 // words of two keys meet by halves, so that a 32-bit AND cuts both keys' nibble
@@ -176,15 +185,14 @@ __device__ __forceinline__ void nibble_columns(const uint32_t (&w)[8], f16x8_t (
     for (int n = 0; n < N; ++n) out[n] = __builtin_bit_cast(f16x8_t, f[n]);
 }
 
-// Queries as B operands of S^T = K Q^T for the operands of nibbles_a (odd
-// elements 1/16). A column's vector is scaled by a power of two to 2^14 .. 2^15 at
-// its largest element; PIECES = 2: x = hi + lo, 11 bits each. Eight elements 8 u
-// and up are one lane's operand of one k-step: lane group g = u / (D / 32), step
+// Queries as B operands of S^T = K Q^T for the operands of nibbles_a<EXACT>. A
+// column's vector is scaled by a power of two to 2^14 .. 2^15 at its largest element
+// (odd elements to 1/16 of that for unsigned codes). PIECES = 1, for bf16 queries: exact;
+// PIECES = 2: x = hi + lo, 11 bits each. Eight elements 8 u and up are one lane's operand of one k-step: lane group g = u / (D / 32), step
 // u % (D / 32).
-//   zero: the accumulator's start, -8 sum x, which turns the unsigned codes into
-//         signed ones
+//   zero: the accumulator's start: -8 sum x turns unsigned codes into signed ones
 //   c:    turns score * key scale into the exponent of 2
-struct KvScaling {
+template <bool EXACT> struct KvScaling {
     int e;
     float sign;
     __device__ __forceinline__ KvScaling(float largest, float scale) {
@@ -192,11 +200,11 @@ struct KvScaling {
         e = some ? 14 - ilogbf(largest) : 0;
         sign = some ? copysignf(1.f, scale) : 0.f;
     }
-    static __device__ __forceinline__ float zero(float sum) { return -8.f * 0x1p-24f * sum; }
+    static __device__ __forceinline__ float zero(float sum) { return EXACT ? 0.f : -8.f * 0x1p-24f * sum; }
     // finite and positive for any finite scale and query
     __device__ __forceinline__ float c(float scale) const {
         if (sign == 0.f) return 1.f;
-        return fminf(fmaxf(ldexpf(fabsf(scale) * 1.4426950408889634f, 24 - e), 0x1p-120f), 0x1p120f);
+        return fminf(fmaxf(ldexpf(fabsf(scale) * 1.4426950408889634f, (EXACT ? 0 : 24) - e), 0x1p-120f), 0x1p120f);
     }
     // one operand (and its share of sum x) from eight elements
     template <int PIECES>
@@ -205,12 +213,13 @@ struct KvScaling {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int el = nibble_slot(i);
-            float y = sign * ldexpf(x[el], (el & 1) ? e - 4 : e);
+            const bool small = !EXACT && (el & 1);
+            float y = sign * ldexpf(x[el], small ? e - 4 : e);
 #pragma unroll
             for (int p = 0; p < PIECES; ++p) {
                 f[p][i] = (_Float16)y;
                 const float r = (float)f[p][i];
-                sum += (el & 1) ? 16.f * r : r;
+                sum += small ? 16.f * r : r;
                 y -= r;
             }
         }
@@ -223,7 +232,7 @@ struct KvScaling {
 template <int D, int NC, int PIECES> struct KvQueries {
     f16x8_t frag[PIECES][NC][D / 32][64];  // [..][k-step][lane]
 };
-template <int D, int NC, int PIECES, typename F>
+template <bool EXACT, int D, int NC, int PIECES, typename F>
 __device__ __forceinline__ void make_queries(KvQueries<D, NC, PIECES>& out, float* zero, float* cs, float scale, F row) {
     constexpr int KW = D / 32, UNITS = D / 8, PER = (UNITS + 15) / 16;
     const int part = threadIdx.x & 15, col = threadIdx.x >> 4;
@@ -241,13 +250,13 @@ __device__ __forceinline__ void make_queries(KvQueries<D, NC, PIECES>& out, floa
         }
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
-        const KvScaling sc(m, scale);
+        const KvScaling<EXACT> sc(m, scale);
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
             const int u = part + 16 * k;
             f16x8_t f[PIECES];
-            sum += sc.pieces<PIECES>(x[k], f);
+            sum += sc.template pieces<PIECES>(x[k], f);
             if (u < UNITS) {
 #pragma unroll
                 for (int p = 0; p < PIECES; ++p) out.frag[p][n][u % KW][16 * (u / KW) + col] = f[p];
@@ -262,11 +271,11 @@ __device__ __forceinline__ void make_queries(KvQueries<D, NC, PIECES>& out, floa
     }
 }
 
-// By the wavefront in registers: a column's four lanes take a quarter each; q is
-// the column's vector or null.
+// By the wavefront in registers, for exact codes: a column's four lanes take a
+// quarter each; q is the column's vector or null.
 template <int D, int PIECES, typename T>
-__device__ __forceinline__ void load_query(const T* q, int g, float scale, f16x8_t (&frag)[PIECES][D / 32], float& zero,
-                                           float& c) {
+__device__ __forceinline__ void load_query(const T* q, int g, float scale, f16x8_t (&frag)[PIECES][D / 32], float& c) {
+    constexpr bool EXACT = true;
     float x[D / 4], m = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
@@ -278,18 +287,14 @@ __device__ __forceinline__ void load_query(const T* q, int g, float scale, f16x8
     for (int i = 0; i < D / 4; ++i) m = fmaxf(m, fabsf(x[i]));
     m = fmaxf(m, __shfl_xor(m, 16));
     m = fmaxf(m, __shfl_xor(m, 32));
-    const KvScaling sc(m, scale);
-    float sum = 0.f;
+    const KvScaling<EXACT> sc(m, scale);
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
         f16x8_t f[PIECES];
-        sum += sc.pieces<PIECES>(x + 8 * w, f);
+        sc.template pieces<PIECES>(x + 8 * w, f);
 #pragma unroll
         for (int p = 0; p < PIECES; ++p) frag[p][w] = f[p];
     }
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    zero = sc.zero(sum);
     c = sc.c(scale);
 }
 
@@ -410,6 +415,9 @@ template <int NC, int PIECES, int NO> struct KvSoftmax {
                     const float p = __builtin_amdgcn_exp2f(z[n][(i + u) >> 2][(i + u) & 3] * c[n]);
                     l[n] += p;
                     y[u] = p * sv[(i + u) >> 2][(i + u) & 3];
+                    // one fp32 value for both pieces: a product fused into one of the conversions
+                    // would round another way and lose the second piece
+                    if constexpr (PIECES == 2) asm("" : "+v"(y[u]));
                 }
 #pragma unroll
                 for (int p = 0; p < PIECES; ++p) {

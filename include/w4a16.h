@@ -465,7 +465,7 @@ int w4_kv_weighted_sum_append(const float* p, const float* v_new, int64_t n, int
  * replays with the contents of that moment; the other fields are host values.
  *   lens [B]: positions sequence b holds, the rows of this call included; each
  *     in [0, capacity], where capacity = table_width * page_size (with a table)
- *     or page_size.
+ *     or page_size; capacity < 2^31 - 64.
  *   starts [B + 1], ascending, or NULL: rows starts[b] .. starts[b + 1] - 1 of
  *     the packed row tensors are sequence b's last positions, row i of its n
  *     at position lens[b] - n + i. NULL: every sequence has rows / B rows
@@ -518,8 +518,8 @@ typedef struct w4_rows {
 } w4_rows;
 
 /*
- * Quantize the batch's rows of keys and values into the cache, in one launch:
- * k, v [rows][Hkv][D], either may be NULL (that half is not written). Codes and
+ * Quantize the batch's rows of keys and values into the cache, in one launch (two
+ * where k and v differ in type): k, v [rows][Hkv][D], either may be NULL (that half is not written). Codes and
  * scales equal w4_kv_quantize's on the same values (a bf16 value counts as the
  * fp32 value it is), bit for bit.
  */
@@ -549,7 +549,8 @@ int w4_kv_read(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows
  * and values are read from the cache: write them first.
  * q [rows][Hq][D] and out [rows][Hq][D], each fp32 or bf16 on its own; Hq a
  * multiple of Hkv; lse fp32 [rows][Hq] contiguous, or NULL; window, sinks >= 0
- * (sinks without a window change nothing); scale finite. workspace: device
+ * (sinks without a window change nothing); scale finite, and |scale * q| under
+ * 2^100. out must not overlap q or the cache. workspace: device
  * memory of at least w4_kv_attention_workspace_bytes(...) bytes for the same
  * cache, batch (its host values), Hq, window and sinks (W4_EWORKSPACE
  * otherwise; may be NULL when that is 0); its contents on entry do not matter,

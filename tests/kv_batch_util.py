@@ -93,7 +93,7 @@ class Batch:
         return [np.concatenate(p) for p in zip(*parts)]
 
 
-def bounds(ref, D, L, vmax, q_dtype, out_dtype):
+def bounds(ref, D, L, vmax, q_dtype, out_dtype, terms=None):
     """Bounds of the errors of out and lse that the arithmetic allows; u = 2^-24, half a step of fp32.
 
     Scores. A bf16 query is exact in the 16-bit format of the products but for what falls under its
@@ -103,6 +103,7 @@ def bounds(ref, D, L, vmax, q_dtype, out_dtype):
     2 D u, the scalings to 4 u, the exponent's argument to 4 u (Z + |m|) with
     the running maximum m, |m| <= Z, and the exponential is good to 2^-22:
         dz = u (Zmax + (2 D + 16) Z) + 2^-22.
+    (`terms`: elements of a query that are not 0, in place of D; adding a zero product is exact.)
     Weights. e^z is off by w = e^(2 dz) - 1 (a row's weight and its maximum's), and sums of L terms by
     L u, in numerator and denominator. The weight times the value's scale enters the second product
     in 16 bits: half a step is 2^-11 of it, 2^-22 in the two pieces that an fp32 query or output
@@ -110,7 +111,7 @@ def bounds(ref, D, L, vmax, q_dtype, out_dtype):
     A bf16 output adds its own half step, 2^-8 of the value."""
     out, lse, A, Z, Zmax = ref
     u = 2.0 ** -24
-    dz = u * (Zmax + (2 * D + 16) * Z) + 2.0 ** -22
+    dz = u * ((Zmax if terms is None else 0) + (2 * (D if terms is None else terms) + 16) * Z) + 2.0 ** -22
     w = np.expm1(2 * dz) + L * u
     piece = 2.0 ** -22 if "f32" in (q_dtype, out_dtype) else 2.0 ** -11
     e = (2 * w + piece + 4 * u)[..., None] * A + L * 2.0 ** -33 * vmax

@@ -156,9 +156,9 @@ def _attend(s, Hq, q_dtype, out_dtype, scale=None, window=0, sinks=0, name="", *
     return got, lse
 
 
-def check(s, got, lse, ref, q_dtype, out_dtype):
+def check(s, got, lse, ref, q_dtype, out_dtype, terms=None):
     vmax = max([np.abs(d).max() for d in s.deq[1] if d.size], default=0.0)
-    e, el = bounds(ref, s.D, max(max(s.lens), 1), vmax, q_dtype, out_dtype)
+    e, el = bounds(ref, s.D, max(max(s.lens), 1), vmax, q_dtype, out_dtype, terms)
     g, l = got.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
     empty = ~np.isfinite(ref[1])
     assert np.array_equal(np.isneginf(l), empty), "rows that see nothing"
@@ -254,6 +254,19 @@ def test_attention_values_of_very_different_scales():
         s.deq[1] = [oracle.kv_dequant(*s.quant[1][0])]
         _attend(s, 4, "f32", "f32", name="vmag")
         _attend(s, 4, "bf16", "bf16", name="vmag")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_fp32_weights_keep_both_pieces(D):
+    """Queries of one element: the scores' bound is some roundings, so that a weight whose second 16-bit
+    piece does not belong to its first (an error of 2^-11 of it) shows in the few keys' sum."""
+    s = Batch([9, 8, 12, 7] * 6, [1] * 24, 2, D, 16, f"pieces.{D}")
+    q = np.zeros((24, 64, D), dtype=np.float32)
+    rng = np.random.default_rng(3)
+    q[np.arange(24)[:, None], np.arange(64)[None], rng.integers(0, D, (24, 64))] = \
+        rng.uniform(-1, 1, (24, 64)).astype(np.float32)
+    got, lse = w4.kv_attention(torch.from_numpy(q).cuda(), s.cache(), s.batch(), scale=0.5, want_lse=True)
+    check(s, got, lse, s.attend(q, 0.5), "f32", "f32", terms=1)
 
 
 def test_attention_growing_scores():
@@ -515,3 +528,49 @@ def test_attention_large_prompts_missing_pages():
 def test_attention_large_prompt_without_a_context():
     """Rows from the first position on: every tile is cut by the causal edge somewhere."""
     _large([700, 611, 640, 655], [700, 611, 640, 655], 2, 32, 128, 16, "bf16", "bf16")
+
+
+def test_large_prompt_in_a_replayed_graph():
+    """Writing, prompt attention and reading back in one captured graph; rows and lengths change on the
+    device between the replays, with eager work in between, and every replay equals the eager calls."""
+    lens, rows, Hkv, G, D = [628, 530, 700, 611], [128, 101, 120, 77], 2, 64, 128
+    s = Batch(lens, rows, Hkv, D, 16, "graphp", vec_dtype="bf16")
+    cache, b = s.cache(), s.batch(max_rows=max(rows), max_len=max(lens))
+    q = torch.empty((s.rows, Hkv * G, D), dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.empty((s.rows, Hkv, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kr, vr = torch.empty_like(k), torch.empty_like(v)
+    out, lse = torch.empty_like(q), torch.empty((s.rows, Hkv * G), dtype=torch.float32, device="cuda")
+    ws = w4.kv_attention_workspace(cache, b, Hkv * G, 300, 4)
+
+    def step():
+        w4.kv_write(k, v, cache, b)
+        w4.kv_attention(q, cache, b, window=300, sinks=4, out=out, lse=lse, workspace=ws)
+        w4.kv_read(cache, b, k=kr, v=vr)
+
+    for t in (q, k, v):
+        t.zero_()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    starts = b.starts.clone()
+    for i in range(4):
+        q.copy_(to_dev(values(tuple(q.shape), f"graphp.q{i}", "bf16"), "bf16"))
+        k.copy_(to_dev(values(tuple(k.shape), f"graphp.k{i}", "bf16"), "bf16"))
+        v.copy_(k)
+        b.lens.copy_(torch.tensor([x - 40 * i for x in lens], dtype=torch.int32))
+        b.starts.copy_(torch.clamp(starts - 3 * i, min=0))
+        out.fill_(3.0), lse.fill_(3.0)
+        g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (out, lse, kr, vr)]
+        out.fill_(3.0), lse.fill_(3.0)
+        step()
+        torch.cuda.synchronize()
+        last = int(b.starts[-1])
+        for x, y in zip(got, (out, lse, kr, vr)):
+            assert torch.equal(x[:last], y[:last])
+        assert (got[0][last:] == 3.0).all() and torch.isfinite(got[0]).all()

@@ -50,6 +50,8 @@ def test_nothing_to_do():
     (_pages(), _batch(max_len=-1), -2), (_pages(), _batch(rows=3), -2),              # 3 rows over 2 sequences
     (_pages(), _batch(width=0), -2), (_pages(), _batch(width=3), -2),                # wider than its stride
     (_pages(), _batch(width=2 ** 28, stride=2 ** 28), -2),                           # positions past 31 bits
+    (_pages(page_size=2 ** 31 - 64, num_pages=2), _batch(table=None), -2),
+    (_pages(num_pages=2 ** 30, page_size=2 ** 26, Hkv=64), _batch(), -2),
     (_pages(), _batch(rows=2 ** 31), -2), (_pages(), _batch(B=2 ** 21, rows=2 ** 21), -2),
     (_pages(kc=None), _batch(), -1), (_pages(vs=None), _batch(), -1), (_pages(), _batch(lens=None), -1),
     (_pages(kc=8), _batch(), -3), (_pages(vs=20), _batch(), -3), (_pages(), _batch(lens=18), -3),
@@ -106,6 +108,10 @@ def test_attention_workspace():
     assert _attend(p, b, q, q) == -5 and _attend(p, b, q, q, ws=16, nbytes=need - 1) == -5
     assert b"workspace" in L.w4_last_error()
     assert _attend(p, b, q, q, ws=8, nbytes=need) == -3
+    # the largest windows and sinks are those that reach past every position
+    for big in (2 ** 31, 2 ** 62, 2 ** 63 - 1):
+        assert L.w4_kv_attention_workspace_bytes(ctypes.byref(p), ctypes.byref(b), 4, big, big) == need
+        assert L.w4_kv_attention_workspace_bytes(ctypes.byref(p), ctypes.byref(b), 4, 0, big) == need
     # a window leaves little to split; a bound on the lengths as well
     assert L.w4_kv_attention_workspace_bytes(ctypes.byref(p), ctypes.byref(b), 4, 64, 4) < need
     short = _batch(width=32, stride=32, max_len=100)
