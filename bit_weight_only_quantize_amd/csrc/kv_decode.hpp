@@ -54,12 +54,17 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
     __shared__ float stat[4][NC * 16][2];  // per wavefront and column: reference, sum
     const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int split = blockIdx.z, head = blockIdx.y, b = blockIdx.x / column_tiles;
+    // Workgroups go to the 8 XCDs in turn: heads side by side, then parts, spread every
+    // sequence over all of them, however the lengths differ.
+    const int split = blockIdx.x / c.Hkv, head = blockIdx.x - split * c.Hkv;
+    const int item = blockIdx.y + blockIdx.z * gridDim.y;  // (sequence, column tile)
+    if (item >= c.B * column_tiles) return;
+    const int b = item / column_tiles;
     const KvSeq s = kv_seq(c, b);
     const int columns = s.n * a.group;  // rows * Hq fits 31 bits
     const int pos0 = s.len - s.n;
     const KvTable table(c, b);
-    for (int ct = blockIdx.x - b * column_tiles; (int64_t)ct * 16 * NC < columns; ct += column_tiles) {
+    for (int ct = item - b * column_tiles; (int64_t)ct * 16 * NC < columns; ct += column_tiles) {
         const int col0 = ct * 16 * NC, col1 = min(col0 + 16 * NC, columns) - 1;
         const int p_lo = pos0 + col0 / a.group, p_hi = pos0 + col1 / a.group;
         const int low_any = a.window > 0 ? max(p_lo, 0) - a.window : -1;
@@ -299,7 +304,8 @@ hipError_t launch_kv_join(const KvPages& c, const KvAttn& a, int splits, hipStre
 
 template <int D, int NC, int PIECES, typename TQ, typename TO>
 hipError_t launch_kv_split_as(const KvPages& c, const KvAttn& a, const KvPlan& p, hipStream_t st) {
-    const dim3 grid((unsigned)((int64_t)p.column_tiles * c.B), (unsigned)c.Hkv, (unsigned)p.splits);
+    const int items = c.B * p.column_tiles, y = items < 32768 ? items : 32768;  // < 2^23
+    const dim3 grid((unsigned)(c.Hkv * p.splits), (unsigned)y, (unsigned)((items + y - 1) / y));
     hipLaunchKernelGGL((kv_split_kernel<D, NC, PIECES, TQ, TO>), grid, dim3(256), 0, st, c, a, p.column_tiles,
                        p.splits);
     hipError_t e = hipGetLastError();
