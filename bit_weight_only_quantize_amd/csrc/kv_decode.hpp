@@ -73,6 +73,13 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
         const int j1 = (int)((unsigned)walk.count * (unsigned)(split + 1) / (unsigned)splits);
         int j = (int)((unsigned)walk.count * (unsigned)split / (unsigned)splits) + wave;
 
+        KvRawQueries<D, NC> raw;
+        raw.load([&](int i) -> const TQ* {
+            const int col = col0 + i, row = col / a.group;
+            return col < columns ? static_cast<const TQ*>(a.q) + (int64_t)(s.first + row) * a.q_row +
+                                       (int64_t)(head * a.group + col - row * a.group) * a.q_head
+                                 : nullptr;
+        });
         // One tile's registers: the next tile's keys are loaded once the scores are
         // formed, its values once the second product is, its page table entries a
         // step before. The other wavefronts of the SIMD cover the rest.
@@ -97,12 +104,7 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
         vals.load(c, half, lane);
         entries(j + 4);
 
-        make_queries<EXACT, D, NC, PIECES>(lds.q, q_zero, q_c, a.scale, [&](int i) -> const TQ* {
-            const int col = col0 + i, row = col / a.group;
-            return col < columns ? static_cast<const TQ*>(a.q) + (int64_t)(s.first + row) * a.q_row +
-                                       (int64_t)(head * a.group + col - row * a.group) * a.q_head
-                                 : nullptr;
-        });
+        raw.template finish<EXACT, PIECES>(lds.q, q_zero, q_c, a.scale);
         __syncthreads();
         f16x8_t q[HOLD ? PIECES : 1][HOLD ? NC : 1][HOLD ? KW : 1];
         if constexpr (HOLD) {

@@ -228,48 +228,65 @@ template <bool EXACT> struct KvScaling {
 };
 
 // By the whole workgroup in LDS: 16 threads a column, 16 NC columns by 256
-// threads; row(col) gives the column's vector or null.
+// threads; row(col) gives the column's vector or null. In two steps, so that the
+// loads are on their way while the first tile is found.
 template <int D, int NC, int PIECES> struct KvQueries {
     f16x8_t frag[PIECES][NC][D / 32][64];  // [..][k-step][lane]
 };
-template <bool EXACT, int D, int NC, int PIECES, typename F>
-__device__ __forceinline__ void make_queries(KvQueries<D, NC, PIECES>& out, float* zero, float* cs, float scale, F row) {
-    constexpr int KW = D / 32, UNITS = D / 8, PER = (UNITS + 15) / 16;
-    const int part = threadIdx.x & 15, col = threadIdx.x >> 4;
+template <int D, int NC> struct KvRawQueries {
+    static constexpr int UNITS = D / 8, PER = (UNITS + 15) / 16;
+    float x[NC][PER][8];
+
+    template <typename F> __device__ __forceinline__ void load(F row) {
+        const int part = threadIdx.x & 15, col = threadIdx.x >> 4;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const auto* q = row(16 * n + col);
-        float x[PER][8], m = 0.f;
+        for (int n = 0; n < NC; ++n) {
+            const auto* q = row(16 * n + col);
 #pragma unroll
-        for (int k = 0; k < PER; ++k) {
+            for (int k = 0; k < PER; ++k) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[k][i] = 0.f;
-            if (q && part + 16 * k < UNITS) load8(q + 8 * (part + 16 * k), x[k]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[k][i]));
-        }
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
-        const KvScaling<EXACT> sc(m, scale);
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            const int u = part + 16 * k;
-            f16x8_t f[PIECES];
-            sum += sc.template pieces<PIECES>(x[k], f);
-            if (u < UNITS) {
-#pragma unroll
-                for (int p = 0; p < PIECES; ++p) out.frag[p][n][u % KW][16 * (u / KW) + col] = f[p];
+                for (int i = 0; i < 8; ++i) x[n][k][i] = 0.f;
+                if (q && part + 16 * k < UNITS) load8(q + 8 * (part + 16 * k), x[n][k]);
             }
         }
+    }
+
+    template <bool EXACT, int PIECES>
+    __device__ __forceinline__ void finish(KvQueries<D, NC, PIECES>& out, float* zero, float* cs, float scale) const {
+        constexpr int KW = D / 32;
+        const int part = threadIdx.x & 15, col = threadIdx.x >> 4;
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor(sum, o);
-        if (part == 0) {
-            zero[16 * n + col] = sc.zero(sum);
-            cs[16 * n + col] = sc.c(scale);
+        for (int n = 0; n < NC; ++n) {
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[n][k][i]));
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+            const KvScaling<EXACT> sc(m, scale);
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int u = part + 16 * k;
+                f16x8_t f[PIECES];
+                sum += sc.template pieces<PIECES>(x[n][k], f);
+                if (u < UNITS) {
+#pragma unroll
+                    for (int p = 0; p < PIECES; ++p) out.frag[p][n][u % KW][16 * (u / KW) + col] = f[p];
+                }
+            }
+            if constexpr (!EXACT) {
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor(sum, o);
+            }
+            if (part == 0) {
+                zero[16 * n + col] = sc.zero(sum);
+                cs[16 * n + col] = sc.c(scale);
+            }
         }
     }
-}
+};
 
 // By the wavefront in registers, for exact codes: a column's four lanes take a
 // quarter each; q is the column's vector or null.
