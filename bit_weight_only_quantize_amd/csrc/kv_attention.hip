@@ -28,8 +28,8 @@ template <int D> hipError_t launch(const KvPages& c, const KvAttn& a, bool q_bf1
 // parts cost two more for the launch that joins them. A tile takes a wavefront about 4850
 // clocks in kv_split_kernel (5900 with D = 256; 6000 in two pieces) and 3500 (5400) in
 // kv_prompt_kernel, for the same columns. Measured, 8 kv heads, bf16, us:
-//   split kernel, a batch of 48 of up to 8192 positions: 77 whole, 50 in two parts (one
-//   round), 58 in three, 62 in eight; two sequences of 131072: 52 in 48 parts, 67 in 16.
+//   split kernel, a batch of 48 of up to 8192 positions: 79 whole, 51 in two parts (one
+//   round), 55 in eight, 69 in sixteen; two of up to 131072: 50 in 48 parts, 67 in 16.
 //   split against prompt kernel (G = 4 unless given): 512 rows 18 / 36, 2048 rows 110 / 104
 //   (D = 256: 197 / 130), 64 rows behind 16384 49 / 55, 512 behind 16384 231 / 202,
 //   8192 rows of 32 heads with G = 1 1030 / 743.

@@ -3,12 +3,17 @@
 // once for a workgroup.
 //
 // A workgroup of eight wavefronts takes 128 NC (row, query head) columns of one
-// (sequence, kv head), 16 NC a wavefront, and walks over the keys in stages of two
-// tiles. Per stage each wavefront turns an eighth of the codes into operands in
-// LDS (one of two buffers, filled a stage ahead) and then takes both tiles for its
-// own columns: unpacking costs an eighth of what it does in kv_split_kernel, and
-// what is left is bound by the softmax's vector instructions next to the matrix
-// cores (two wavefronts a SIMD, one's softmax beside the other's products).
+// (sequence, kv head), 16 NC a wavefront, and walks over the keys in stages of
+// four tiles (two with D = 256). Per stage each wavefront turns its share of the codes
+// into operands in LDS (one of two buffers, filled a stage ahead) and then takes
+// every tile for its own columns: unpacking costs an eighth of what it does in
+// kv_split_kernel. The causal edge makes the last columns the longest: they go first.
+//
+// A tile takes each wavefront about 3500 clocks, two wavefronts a SIMD; the matrix
+// cores work 30% of the time and the vector unit 60%, with a wavefront's phases waiting
+// on one another (scores 380, softmax 1000 to 1250, second product 390, its share
+// of the filling 500, barriers 200 to 900). 8192 rows of 32 heads of 128: 745 us, 740
+// TFLOP/s over the causal pairs, where a library's bf16 product of 8192^3 runs at 1205.
 #pragma once
 
 #include "kv_decode.hpp"
