@@ -469,7 +469,17 @@ def kv_weighted_sum_append(p: torch.Tensor, v_new: torch.Tensor, codes: torch.Te
 _ROW_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
-class KVPages:
+class _Fixed:
+    """Attributes are set once: the C descriptors hold the tensors' addresses."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} is fixed: change the tensor in place or make a new "
+                                 f"{type(self).__name__}")
+        object.__setattr__(self, name, value)
+
+
+class KVPages(_Fixed):
     """The pool of a batched INT4 KV cache: codes uint8 [pages][Hkv][page_size][D / 2] and scales
     fp32 [pages][Hkv][page_size] of the keys and of the values (w4_kv_pages in include/w4a16.h).
     The tensors are the caller's; kv_pages allocates them."""
@@ -504,7 +514,7 @@ def kv_pages(num_pages: int, Hkv: int, page_size: int, D: int = KV_HEAD_DIM, dev
     return KVPages(codes[0], scales[0], codes[1], scales[1])
 
 
-class KVBatch:
+class KVBatch(_Fixed):
     """Which rows and pages belong to which sequence (w4_kv_batch in include/w4a16.h).
 
     lens int32 [B] (device): positions each sequence holds, the rows of the call included.
@@ -513,7 +523,8 @@ class KVBatch:
     are starts[b] .. starts[b + 1] - 1; without it every sequence has rows / B rows. rows: packed
     rows in all (default B, one a sequence); max_rows, max_len: the most rows and positions of one
     sequence, which shape the launch (default: as many as there can be). The device tensors are
-    read when the kernels run: a captured graph follows what they hold then."""
+    read when the kernels run: a captured graph follows what they hold then. They are changed in
+    place (batch.lens.add_(1)), never replaced."""
 
     def __init__(self, lens: torch.Tensor, table: Optional[torch.Tensor] = None,
                  starts: Optional[torch.Tensor] = None, rows: Optional[int] = None,

@@ -193,6 +193,14 @@ def test_attention_one_token_lengths(L):
     _attend(s, 8, "f32", "f32", name=f"l{L}")
 
 
+def test_descriptors_keep_their_tensors():
+    s = Batch([5], [1], 1, 64, 16, "fixed")
+    cache, b = s.cache(), s.batch()
+    for obj, name in ((b, "lens"), (b, "table"), (b, "starts"), (b, "rows"), (cache, "k_codes"), (cache, "v_scales")):
+        with pytest.raises(AttributeError):
+            setattr(obj, name, getattr(obj, name))
+
+
 @pytest.mark.parametrize("lens,rows,page", [
     ([1], [1], 0), ([2], [2], 16), ([64], [64], 0), ([65], [65], 16), ([200], [200], 32),
     ([300, 40, 0, 129], [17, 40, 2, 1], 16),                   # a slot with rows and no position
