@@ -396,7 +396,7 @@ template <int NC, int PIECES, int NO> struct KvSoftmax {
             float fv = 1.f;
             big = wave_max(big);
             if (big >= sv_max && big > 0.f) {
-                const int e = min(max(ilogbf(big), -110), 110);
+                const int e = min(max(ilogbf(big), -118), 127);  // 2^(kBoost - e) is a normal float
                 const float r = ldexpf(1.f, kBoost - e);
                 fv = rv > 0.f ? r / rv : 0.f;  // powers of two
                 rv = r;

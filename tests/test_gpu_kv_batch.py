@@ -264,6 +264,19 @@ def test_attention_values_of_very_different_scales():
         _attend(s, 4, "bf16", "bf16", name="vmag")
 
 
+@pytest.mark.parametrize("power", [-120, -60, 60, 110, 122])
+def test_attention_values_near_the_ends_of_the_type(power):
+    """Values up to 2^125 and down to the least normal scales: the running power of two follows them."""
+    s = Batch([90], [2], 1, 128, 16, f"vend.{power}")
+    v = s.x[1][0] * np.float32(2.0 ** power)
+    v[:, :40] *= np.float32(2.0 ** (-4 if power < 0 else -20))
+    s.quant[1] = [oracle.kv_quantize(v)]
+    s.deq[1] = [oracle.kv_dequant(*s.quant[1][0])]
+    _attend(s, 4, "f32", "f32", name="vend")
+    if power < 100:
+        _attend(s, 4, "bf16", "bf16", name="vend")
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attention_fp32_weights_keep_both_pieces(D):
     """Queries of one element: the scores' bound is some roundings, so that a weight whose second 16-bit
