@@ -193,6 +193,16 @@ def test_attention_one_token_lengths(L):
     _attend(s, 8, "f32", "f32", name=f"l{L}")
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("L", [1, 2, 3, 5, 15, 17, 18, 19, 33, 47, 66])
+def test_attention_up_to_the_last_position_of_the_pool(L, D):
+    """Caches that hold no position more than their sequences: the last tile ends inside the pool's memory,
+    at any remainder of the 16 keys and 4 scales that are read together."""
+    s = Batch([L, L], [1, min(L, 4)], 1, D, 0, f"end.{L}.{D}")
+    s.size = L
+    _attend(s, 3, "f32", "f32", name=f"end{L}")
+
+
 def test_descriptors_keep_their_tensors():
     s = Batch([5], [1], 1, 64, 16, "fixed")
     cache, b = s.cache(), s.batch()
