@@ -210,7 +210,7 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
             // this wavefront's share of the columns, d consecutive per lane
             // (its own reference as stored: an fma of the product with -top would not give 0)
             const float own = stat[wave][16 * n + l16][0];
-            const float f = own > -INFINITY && sm.rv > 0.f ? __builtin_amdgcn_exp2f(own - top) / sm.rv : 0.f;
+            const float f = own > -INFINITY ? __builtin_amdgcn_exp2f(own - top) / sm.rv[n] : 0.f;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll

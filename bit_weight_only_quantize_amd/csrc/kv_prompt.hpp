@@ -270,7 +270,7 @@ __global__ __launch_bounds__(512, 2) void kv_prompt_kernel(KvPages c, KvAttn a, 
             const int row = s.first + col / a.group, h = head * a.group + col % a.group;
             const bool some = sm.thr[n] > -INFINITY;
             const float top = some ? sm.mx[n] * qc[n] : -INFINITY;
-            float f = some && sm.rv > 0.f ? 1.f / sm.rv : 0.f;
+            float f = some ? 1.f / sm.rv[n] : 0.f;
             if (splits > 1) {
                 float* w = static_cast<float*>(a.work) +
                            (((int64_t)row * a.Hq + h) * splits + split) * kv_partial_floats(D);

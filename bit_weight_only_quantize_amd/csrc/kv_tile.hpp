@@ -321,28 +321,42 @@ __device__ __forceinline__ void load_query(const T* q, int g, float scale, f16x8
 // follows the maximum lazily, once a weight would pass 2^kLift, so that most
 // tiles scale nothing.
 constexpr float kLift = 4.f;
-// Weights times value scales enter the second product as 16-bit floats. Value
-// scales are taken relative to 2^e, e the exponent of the largest so far,
-// which is raised once a scale reaches 8 * 2^e; with 2^kBoost on top the operand
-// stays below 2^(kLift + 3 + kBoost) = 2^15, and what the format's least step
-// drops is 2^-33 of the largest value.
+// Weights times value scales, y = p s_v, enter the second product as 16-bit floats, times
+// a power of two of the column's own, rv. It is set where the reference moves, or where a y
+// would reach 2^15, so that the largest y so far stands at 2^kBoost: what the format's
+// least step drops is 2^-33 of the largest y of the column. Values that a column does not
+// see, or gives no weight, do not move it: a row's result depends on nothing but what it sees.
 constexpr int kBoost = 8;
+constexpr float kTop = 15.f;  // log2 of what y rv stays below
+
+// p times a value scale, 0 where p is 0: a hidden key's scale may be infinite or NaN. (The
+// instruction v_mul_legacy_f32 by the intrinsic's name: in inline assembly the compiler would not keep it
+// a cycle away from the exponential before it.)
+__device__ float kv_weigh(float p, float scale) __asm("llvm.amdgcn.fmul.legacy");
+
+// The largest of a column's four lanes (l, l ^ 16, l ^ 32, l ^ 48), on each of them.
+__device__ __forceinline__ float column_max(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
 
 // One wavefront's NC column tiles; NO operands of 16 output elements each.
 template <int NC, int PIECES, int NO> struct KvSoftmax {
     float mx[NC], thr[NC], l[NC];  // thr -inf: nothing seen so far; l: this lane's keys only
+    float rv[NC];                  // 2^-119 .. 2^126: it and its inverse are normal
     f32v4_t o[NC][NO];
-    float rv, sv_max;  // 2^(kBoost - e), 8 * 2^e
 
     __device__ __forceinline__ void start() {
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
             thr[n] = -INFINITY;
             mx[n] = l[n] = 0.f;
+            rv[n] = 0x1p126f;
 #pragma unroll
             for (int i = 0; i < NO; ++i) o[n][i] = f32v4_t{0.f, 0.f, 0.f, 0.f};
         }
-        rv = sv_max = 0.f;
     }
 
     // z: scores in, relative to mx out
@@ -380,34 +394,29 @@ template <int NC, int PIECES, int NO> struct KvSoftmax {
     // Weights of a tile, as operands of the second product.
     __device__ __forceinline__ void weights(f32v4_t (&z)[NC][2], const f32v4_t (&vs)[2], const float (&c)[NC],
                                             f16x8_t (&pf)[NC][PIECES]) {
-        float top[NC];
+        float top[NC], big = fabsf(vs[0][0]);
         bool move = false;
+#pragma unroll
+        for (int i = 1; i < 8; ++i) big = fmaxf(big, fabsf(vs[i >> 2][i & 3]));
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
             top[n] = z[n][0][0];
 #pragma unroll
             for (int i = 1; i < 8; ++i) top[n] = fmaxf(top[n], z[n][i >> 2][i & 3]);
-            move = move || top[n] > thr[n];
+            // weights are at most 2^kLift where the reference stays
+            move = move | (top[n] > thr[n]) | (big * rv[n] >= 0x1p11f);
         }
-        float big = vs[0][0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) big = fmaxf(big, vs[i >> 2][i & 3]);
-        if (__builtin_amdgcn_ballot_w64(move || big >= sv_max) != 0) {  // rarely
-            float fv = 1.f;
-            big = wave_max(big);
-            if (big >= sv_max && big > 0.f) {
-                const int e = min(max(ilogbf(big), -118), 127);  // 2^(kBoost - e) is a normal float
-                const float r = ldexpf(1.f, kBoost - e);
-                fv = rv > 0.f ? r / rv : 0.f;  // powers of two
-                rv = r;
-                sv_max = ldexpf(8.f, e);
-            }
+        if (__builtin_amdgcn_ballot_w64(move) != 0) {  // rarely, but where values of little weight are large
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
-                float t = fmaxf(top[n], __shfl_xor(top[n], 16));
-                t = fmaxf(t, __shfl_xor(t, 32));
-                float f = 1.f;
-                if (t > thr[n]) {  // alike on the column's four lanes
+                // the largest weight times the largest scale of the lane's keys bounds their y
+                const bool far = fmaf(top[n], c[n], __builtin_amdgcn_logf(big * rv[n])) >= kTop;
+                if (__builtin_amdgcn_ballot_w64(top[n] > thr[n] | far) == 0) continue;
+                // decisions are alike on the column's four lanes, and do not depend on other columns
+                const float t = column_max(top[n]);
+                float f = 1.f, fv = 1.f;
+                const bool moved = t > thr[n];
+                if (moved) {
                     const float to = mx[n] + t, by = to - mx[n];
                     f = thr[n] > -INFINITY ? __builtin_amdgcn_exp2f(-by * c[n]) : 0.f;
                     mx[n] = to;
@@ -415,13 +424,26 @@ template <int NC, int PIECES, int NO> struct KvSoftmax {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) z[n][i >> 2][i & 3] -= by;
                 }
+                float y = 0.f, cn = c[n];
+                asm("" : "+v"(cn));  // other exponentials than those below, which would wait in registers
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    y = fmaxf(y, kv_weigh(__builtin_amdgcn_exp2f(z[n][i >> 2][i & 3] * cn), fabsf(vs[i >> 2][i & 3])));
+                y = column_max(y);
+                if (moved || y * rv[n] >= 0x1p15f) {
+                    // the largest so far: 2^kBoost / rv when rv was set, less what the reference moved
+                    const float inv = __uint_as_float((254u << 23) - __float_as_uint(rv[n]));  // 1 / rv
+                    const int e = min(max(ilogbf(fmaxf((0x1p8f * inv) * f, y)), -118), 127);
+                    const float r = ldexpf(1.f, kBoost - e);
+                    fv = fminf(r * inv, 0x1p127f);  // a power of two
+                    rv[n] = r;
+                }
                 l[n] *= f;
                 f *= fv;
 #pragma unroll
                 for (int i = 0; i < NO; ++i) o[n][i] *= f;
             }
         }
-        const f32v4_t sv[2] = {vs[0] * rv, vs[1] * rv};
 #pragma unroll
         for (int n = 0; n < NC; ++n)
 #pragma unroll
@@ -431,7 +453,7 @@ template <int NC, int PIECES, int NO> struct KvSoftmax {
                 for (int u = 0; u < 2; ++u) {
                     const float p = __builtin_amdgcn_exp2f(z[n][(i + u) >> 2][(i + u) & 3] * c[n]);
                     l[n] += p;
-                    y[u] = p * sv[(i + u) >> 2][(i + u) & 3];
+                    y[u] = kv_weigh(p, vs[(i + u) >> 2][(i + u) & 3]) * rv[n];
                     // one fp32 value for both pieces: a product fused into one of the conversions
                     // would round another way and lose the second piece
                     if constexpr (PIECES == 2) asm("" : "+v"(y[u]));

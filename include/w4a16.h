@@ -555,6 +555,9 @@ int w4_kv_read(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows
  * cache, batch (its host values), Hq, window and sinks (W4_EWORKSPACE
  * otherwise; may be NULL when that is 0); its contents on entry do not matter,
  * on return they are unspecified. Calls sharing a workspace must not overlap.
+ * A row's result depends on nothing but what the row sees: keys and values hidden
+ * from it may be of any size, infinite or NaN. Among those it sees, a weight times
+ * value scale under 2^-33 of the row's largest is dropped.
  * Softmax statistics and sums are fp32; the products run on the matrix cores
  * with the codes as exact 16-bit integers, a bf16 query exact and an fp32 one
  * in two pieces of 11 bits. Deterministic for given arguments; max_rows and

@@ -1,0 +1,160 @@
+"""GPU tests of the batched INT4 KV cache at unusual values: values and scales that a row does not
+see or gives no weight, infinities and NaN, magnitudes near the ends of the types."""
+import numpy as np
+import pytest
+import torch
+
+import bit_weight_only_quantize_amd as w4
+import oracle
+from kv_batch_util import DT, Batch, bounds, to_dev, values
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+
+
+def check_rows(s, q, got, lse, q_dtype, out_dtype, scale=None, terms=None, rows=None):
+    """Causal rows (default: all) against the oracle. The weights' 16-bit format: a weight times value scale is
+    off by 2^-25 of the format's unit where the column's largest is 2^8 of it at least, so by 2^-33 of that
+    for each key, times codes of up to 8: of the largest p_t * 8 * scale_t that the row itself sees."""
+    sc = float(np.float32(s.D ** -0.5 if scale is None else scale))
+    pick = list(range(s.rows)) if rows is None else list(rows)
+    refs, tops = [], []
+    for r in pick:
+        b = int(np.searchsorted(s.first, r, side="right")) - 1
+        t = np.arange(s.lens[b] - s.n[b] + r - s.first[b] + 1)
+        k, v, vs = s.deq[0][b][:, t], s.deq[1][b][:, t], s.quant[1][b][1][:, t].astype(np.float64)
+        refs.append(oracle.kv_attention(q[r][None], k, v, sc))
+        g = np.arange(q.shape[1]) // (q.shape[1] // s.Hkv)
+        z = sc * (k[g] @ q[r].astype(np.float64)[..., None])[..., 0]
+        tops.append((np.exp(z - refs[-1][1][0][:, None]) * 8 * vs[g]).max(1))
+    ref = [np.concatenate(x) for x in zip(*refs)]
+    e, el = bounds(ref, s.D, max(s.lens), np.stack(tops)[..., None], q_dtype, out_dtype, terms)
+    g, l = got[pick].float().cpu().numpy().astype(np.float64), lse[pick].cpu().numpy().astype(np.float64)
+    assert np.isfinite(g).all() and np.isfinite(l).all()
+    worst, lw = (np.abs(g - ref[0]) / e).max(), (np.abs(l - ref[1]) / el).max()
+    print(f"[kv values] out {worst:.3f} lse {lw:.3f} of the bounds", flush=True)
+    assert worst <= 1.0 and lw <= 1.0
+
+
+def set_values(s, scales, b=0):
+    """Sequence b's value scales times `scales` [L] (before the cache is made)."""
+    c, old = s.quant[1][b]
+    s.quant[1][b] = (c, (old * np.asarray(scales, dtype=np.float64)[None]).astype(np.float32))
+    s.deq[1][b] = oracle.kv_dequant(*s.quant[1][b])
+
+
+def set_scores(s, q, z, b=0):
+    """Sequence b's keys such that a row with q = 1 in element 0 and 0 elsewhere scores about z[t] (scale 1)."""
+    k = np.zeros((s.Hkv, s.lens[b], s.D), dtype=np.float32)
+    k[:, :, 0] = np.asarray(z, dtype=np.float32)[None]
+    s.quant[0][b] = oracle.kv_quantize(k)
+    s.deq[0][b] = oracle.kv_dequant(*s.quant[0][b])
+    q[...] = 0
+    q[..., 0] = 1
+
+
+SPLIT = dict(lens=[50, 40], rows=[12, 1], Hkv=2, G=5, page=16)         # few columns, whole
+PARTS = dict(lens=[5003, 700], rows=[3, 2], Hkv=1, G=4, page=64)       # few columns, keys in parts
+PROMPT = dict(lens=[628, 530, 700, 611], rows=[128, 101, 120, 77], Hkv=2, G=64, page=16)   # many columns
+SHARED = dict(lens=[5000, 4700, 4900, 4850], rows=[1000, 900, 1000, 800], Hkv=4, G=8, page=32)   # four rows a wavefront
+PROMPT_PARTS = dict(lens=[9001], rows=[130], Hkv=1, G=64, page=64)
+
+
+def make(shape, D, name, q_dtype="f32"):
+    s = Batch(shape["lens"], shape["rows"], shape["Hkv"], D, shape["page"], name)
+    return s, values((s.rows, shape["Hkv"] * shape["G"], D), name + ".q", q_dtype, seed=2)
+
+
+def attend(s, cache, q, q_dtype, out_dtype, **kw):
+    b = s.batch(max_rows=max(s.n), max_len=max(s.lens))
+    out = torch.full(q.shape, 9.0, dtype=DT[out_dtype], device="cuda")
+    return w4.kv_attention(to_dev(q, q_dtype), cache, b, out=out, want_lse=True, **kw)
+
+
+def same_bits(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+# ---------------------------------------------------------------- values without weight
+@pytest.mark.parametrize("factor", [2.0 ** 20, 2.0 ** 40, 2.0 ** 100, INF, NAN])
+@pytest.mark.parametrize("D,types", [(64, ("f32", "f32")), (128, ("bf16", "bf16")), (256, ("f32", "bf16"))])
+@pytest.mark.parametrize("shape", [SPLIT, PARTS, SHARED], ids=["split", "parts", "prompt"])
+def test_later_rows_do_not_reach_earlier_ones(shape, D, types, factor):
+    """A key and value of any scale at a later row's position: the rows before it keep their bits."""
+    s, q = make(shape, D, f"later.{D}", types[0])
+    want = attend(s, s.cache(), q, *types)
+    cache, before = s.cache(), []
+    for b in range(s.B):
+        n, L = s.n[b], s.lens[b]
+        i = n - 1 - (n - 1) // 2                              # the row whose key and value change
+        p, o = s.place(b, L - n + i)
+        for scales in (cache.k_scales, cache.v_scales):
+            scales[int(p), :, int(o)] *= factor
+        before += range(s.first[b], s.first[b] + i)
+    got = attend(s, cache, q, *types)
+    assert len(before) > 0
+    for x, y in zip(got, want):
+        assert torch.isfinite(x[before]).all() and same_bits(x[before], y[before])
+
+
+@pytest.mark.parametrize("factor", [2.0 ** 20, 2.0 ** 100, INF, NAN])
+@pytest.mark.parametrize("D,types", [(64, ("f32", "f32")), (128, ("bf16", "bf16"))])
+@pytest.mark.parametrize("shape,window", [(SPLIT, 9), (SHARED, 700)], ids=["split", "prompt"])
+def test_values_behind_the_window_do_not_reach_its_rows(shape, window, D, types, factor):
+    """A key and value that the window of the first rows still holds: the rows past it keep their bits."""
+    s, q = make(shape, D, f"behind.{D}", types[0])
+    mask = dict(window=window, sinks=2)
+    want = attend(s, s.cache(), q, *types, **mask)
+    cache, past = s.cache(), []
+    for b in range(s.B):
+        n, first = s.n[b], s.lens[b] - s.n[b]
+        p, o = s.place(b, first)                               # seen by the first `window` rows
+        for scales in (cache.k_scales, cache.v_scales):
+            scales[int(p), :, int(o)] *= factor
+        past += range(s.first[b] + window, s.first[b] + n)
+    got = attend(s, cache, q, *types, **mask)
+    for x, y in zip(got, want):
+        assert torch.isfinite(x[past]).all() and same_bits(x[past], y[past])
+
+
+@pytest.mark.parametrize("types", [("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("ratio", [2.0 ** 16, 2.0 ** 24, 2.0 ** 40, 2.0 ** 60])
+def test_large_values_without_weight(ratio, types):
+    """Visible values `ratio` times the others under a weight of e^-70: the rest keeps its precision."""
+    for at in (0, 37, 99):
+        s, q = make(dict(lens=[100], rows=[1], Hkv=1, G=3, page=16), 64, f"light.{at}")
+        z = np.random.default_rng(1).uniform(-1, 1, 100)
+        z[at] = -70
+        set_scores(s, q, z)
+        set_values(s, np.where(np.arange(100) == at, ratio, 1.0))
+        got, lse = attend(s, s.cache(), q, *types, scale=1.0)
+        check_rows(s, q, got, lse, *types, scale=1.0, terms=1)
+
+
+@pytest.mark.parametrize("types", [("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("lens,rows,G", [([300], [2], 3), ([5000], [1], 2), ([700] * 4, [160] * 4, 64)],
+                         ids=["split", "parts", "prompt"])
+@pytest.mark.parametrize("fall", [30, 100])
+def test_values_that_shrink_while_their_weights_grow(fall, lens, rows, G, types):
+    """Scores grow by 84 along the sequence (weights by 2^121) and values shrink by 2^fall: what counts at
+    the end is far under the first values."""
+    s, q = make(dict(lens=lens, rows=rows, Hkv=1, G=G, page=16), 64, f"shrink.{fall}.{lens}")
+    L = lens[0]
+    for b in range(s.B):
+        set_scores(s, q, np.linspace(-84, 0, L), b)
+        set_values(s, np.exp2(np.linspace(0, -fall, L)), b)
+    got, lse = attend(s, s.cache(), q, *types, scale=1.0)
+    pick = [int(s.first[b]) + i for b in range(s.B) for i in {0, s.n[b] // 2, s.n[b] - 1}]
+    check_rows(s, q, got, lse, *types, scale=1.0, terms=1, rows=pick)
+
+
+@pytest.mark.parametrize("power,ahead", [(-115, 0), (-60, 30), (0, 30), (110, 0), (110, 30)])
+def test_values_that_begin_with_zeros(power, ahead):
+    """The first 70 values are zeros, their scores `ahead` of the others; the rest, of any magnitude, enters
+    all the same."""
+    s, q = make(dict(lens=[200], rows=[2], Hkv=1, G=3, page=16), 64, f"zeros.{power}")
+    set_scores(s, q, np.where(np.arange(200) < 70, ahead, 0.0))
+    set_values(s, np.where(np.arange(200) < 70, 0.0, 2.0 ** power))
+    got, lse = attend(s, s.cache(), q, "f32", "f32", scale=1.0)
+    check_rows(s, q, got, lse, "f32", "f32", scale=1.0, terms=1)
