@@ -39,8 +39,9 @@ constexpr int kMaxSplits = 64;
 KvPlan kv_plan(const KvPages& c, int D, int group, int pieces, int64_t max_rows, int64_t max_len, int64_t window,
                int64_t sinks);
 
-// Partial results of a part: out[D] unnormalized, then the exponent's reference
-// (base 2) and the sum.
+// Partial results of a part: out[D] over its own keys, then the exponent's reference
+// (base 2) and the sum. Results are divided by their sums before anything is added to
+// them: sums of weights times values could pass the end of fp32 where their mean does not.
 __host__ __device__ constexpr int kv_partial_floats(int D) { return D + 4; }
 inline size_t kv_partial_bytes(int64_t vectors, int splits, int D) {
     return (size_t)vectors * splits * kv_partial_floats(D) * sizeof(float);
@@ -210,13 +211,13 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
             // this wavefront's share of the columns, d consecutive per lane
             // (its own reference as stored: an fma of the product with -top would not give 0)
             const float own = stat[wave][16 * n + l16][0];
-            const float f = own > -INFINITY ? __builtin_amdgcn_exp2f(own - top) / sm.rv[n] : 0.f;
+            const float f = own > -INFINITY ? __builtin_amdgcn_exp2f(own - top) / sum : 0.f, inv = 1.f / sm.rv[n];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int i = 0; i < VW * VN; i += 4)
                     *reinterpret_cast<f32v4_t*>(&lds.part[wave][l16][(4 * g + r) * (VW * VN) + i]) =
-                        f32v4_t{sm.o[n][i][r], sm.o[n][i + 1][r], sm.o[n][i + 2][r], sm.o[n][i + 3][r]} * f;
+                        f32v4_t{sm.o[n][i][r], sm.o[n][i + 1][r], sm.o[n][i + 2][r], sm.o[n][i + 3][r]} * f * inv;
             __syncthreads();
             // 16 threads a column add the four and store
             const int cl = threadIdx.x >> 4, col = col0 + 16 * n + cl;
@@ -244,9 +245,6 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
                         *reinterpret_cast<f32v4_t*>(w + e0 + i) = f32v4_t{y[i], y[i + 1], y[i + 2], y[i + 3]};
                     if (e0 == 0) *reinterpret_cast<f32v4_t*>(w + D) = f32v4_t{ctop, csum, 0.f, 0.f};
                 } else {
-                    const float inv = csum > 0.f ? 1.f / csum : 0.f;
-#pragma unroll
-                    for (int i = 0; i < E; ++i) y[i] *= inv;
                     store_run<E>(static_cast<TO*>(a.out) + row * a.out_row + h * a.out_head + e0, y);
                     if (a.lse && e0 == 0)
                         a.lse[(int64_t)row * a.Hq + h] = csum > 0.f ? (ctop + __builtin_amdgcn_logf(csum)) * 0.6931471805599453f : -INFINITY;
@@ -283,14 +281,14 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvPages c, KvAttn a, int s
     const float m = lane < splits ? ms[0] : -INFINITY;
     const float top = wave_max(m);
     const float f = m > -INFINITY ? __builtin_amdgcn_exp2f(m - top) : 0.f;
-    const float sum = group_sum<64>(f * ms[1]);
+    const float sum = group_sum<64>(f * ms[1]), share = sum > 0.f ? f * ms[1] / sum : 0.f;
     f32v4_t y = {0.f, 0.f, 0.f, 0.f};
     for (int base = 0; base < splits; base += SIDE * kAhead) {
         if (base) load(base);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const int i = base + SIDE * k + side;
-            const float fi = __shfl(f, min(i, 63));
+            const float fi = __shfl(share, min(i, 63));
             y += x[k] * (i < splits ? fi : 0.f);
         }
     }
@@ -298,9 +296,8 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvPages c, KvAttn a, int s
     for (int o = LANES; o < 64; o <<= 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] += __shfl_xor(y[e], o);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
     if (side == 0) {
-        const float r[4] = {y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv};
+        const float r[4] = {y[0], y[1], y[2], y[3]};
         store_run<4>(static_cast<TO*>(a.out) + row * a.out_row + h * a.out_head + e0, r);
     }
     if (a.lse && lane == 0) a.lse[v] = sum > 0.f ? (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f : -INFINITY;

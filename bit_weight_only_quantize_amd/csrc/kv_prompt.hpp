@@ -270,7 +270,7 @@ __global__ __launch_bounds__(512, 2) void kv_prompt_kernel(KvPages c, KvAttn a, 
             const int row = s.first + col / a.group, h = head * a.group + col % a.group;
             const bool some = sm.thr[n] > -INFINITY;
             const float top = some ? sm.mx[n] * qc[n] : -INFINITY;
-            float f = some ? 1.f / sm.rv[n] : 0.f;
+            const float f = sm.l[n] > 0.f ? 1.f / sm.l[n] : 0.f, inv = 1.f / sm.rv[n];
             if (splits > 1) {
                 float* w = static_cast<float*>(a.work) +
                            (((int64_t)row * a.Hq + h) * splits + split) * kv_partial_floats(D);
@@ -279,16 +279,15 @@ __global__ __launch_bounds__(512, 2) void kv_prompt_kernel(KvPages c, KvAttn a, 
 #pragma unroll
                     for (int i = 0; i < NO; i += 4)
                         *reinterpret_cast<f32v4_t*>(w + (4 * g + r) * NO + i) =
-                            f32v4_t{sm.o[n][i][r], sm.o[n][i + 1][r], sm.o[n][i + 2][r], sm.o[n][i + 3][r]} * f;
+                            f32v4_t{sm.o[n][i][r], sm.o[n][i + 1][r], sm.o[n][i + 2][r], sm.o[n][i + 3][r]} * f * inv;
                 if (g == 0) *reinterpret_cast<f32v4_t*>(w + D) = f32v4_t{top, sm.l[n], 0.f, 0.f};
                 continue;
             }
-            f = sm.l[n] > 0.f ? f / sm.l[n] : 0.f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 float y[NO];
 #pragma unroll
-                for (int i = 0; i < NO; ++i) y[i] = sm.o[n][i][r] * f;
+                for (int i = 0; i < NO; ++i) y[i] = sm.o[n][i][r] * f * inv;
                 store_run<NO>(static_cast<TO*>(a.out) + row * a.out_row + h * a.out_head + (4 * g + r) * NO, y);
             }
             if (a.lse && g == 0)

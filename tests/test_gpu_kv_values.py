@@ -158,3 +158,25 @@ def test_values_that_begin_with_zeros(power, ahead):
     set_values(s, np.where(np.arange(200) < 70, 0.0, 2.0 ** power))
     got, lse = attend(s, s.cache(), q, "f32", "f32", scale=1.0)
     check_rows(s, q, got, lse, "f32", "f32", scale=1.0, terms=1)
+
+
+# ---------------------------------------------------------------- magnitudes
+@pytest.mark.parametrize("shape", [
+    dict(lens=[4000], rows=[1], Hkv=1, G=2, page=16, max_len=1),       # whole
+    dict(lens=[4000], rows=[1], Hkv=1, G=2, page=16, max_len=4000),    # in parts
+    dict(lens=[3000] * 4, rows=[100] * 4, Hkv=2, G=64, page=16, max_len=3000),
+    dict(lens=[9001], rows=[130], Hkv=1, G=64, page=64, max_len=9001),
+], ids=["whole", "parts", "prompt", "prompt in parts"])
+@pytest.mark.parametrize("power", [115, 125, -121])
+def test_sums_of_large_and_small_values_of_one_sign(shape, power):
+    """Thousands of values of one sign near the ends of fp32 under equal weights: the mean, though their
+    sum would pass the type's end."""
+    s, q = make(shape, 64, f"mean.{power}")
+    for b in range(s.B):
+        set_scores(s, q, np.zeros(s.lens[b]), b)
+        v = (np.abs(s.x[1][b]).clip(0.5, 1) * 2.0 ** power).astype(np.float32)
+        s.quant[1][b] = oracle.kv_quantize(v)
+        s.deq[1][b] = oracle.kv_dequant(*s.quant[1][b])
+    b = s.batch(max_rows=max(s.n), max_len=shape["max_len"])
+    got, lse = w4.kv_attention(torch.from_numpy(q).cuda(), s.cache(), b, want_lse=True)
+    check_rows(s, q, got, lse, "f32", "f32", terms=1, rows=[0, s.rows // 2, s.rows - 1])
