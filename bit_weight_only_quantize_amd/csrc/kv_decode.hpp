@@ -194,7 +194,7 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
 #pragma unroll
         for (int n = 0; n < NC; ++n)
             if (g == 0) {
-                stat[wave][16 * n + l16][0] = sm.thr[n] > -INFINITY ? sm.mx[n] * qc[n] : -INFINITY;
+                stat[wave][16 * n + l16][0] = sm.reference(n, qc[n]);
                 stat[wave][16 * n + l16][1] = sm.l[n];
             }
         __syncthreads();
@@ -206,12 +206,12 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const float mw = stat[w][16 * n + l16][0];
-                sum += mw > -INFINITY ? stat[w][16 * n + l16][1] * __builtin_amdgcn_exp2f(mw - top) : 0.f;
+                sum += mw == -INFINITY ? 0.f : stat[w][16 * n + l16][1] * __builtin_amdgcn_exp2f(mw - top);
             }
             // this wavefront's share of the columns, d consecutive per lane
             // (its own reference as stored: an fma of the product with -top would not give 0)
             const float own = stat[wave][16 * n + l16][0];
-            const float f = own > -INFINITY ? __builtin_amdgcn_exp2f(own - top) / sum : 0.f, inv = 1.f / sm.rv[n];
+            const float f = own == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(own - top) / sum, inv = 1.f / sm.rv[n];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -247,7 +247,7 @@ __global__ __launch_bounds__(256, (NC == 1 && D <= 128) ? 3 : 2) void kv_split_k
                 } else {
                     store_run<E>(static_cast<TO*>(a.out) + row * a.out_row + h * a.out_head + e0, y);
                     if (a.lse && e0 == 0)
-                        a.lse[(int64_t)row * a.Hq + h] = csum > 0.f ? (ctop + __builtin_amdgcn_logf(csum)) * 0.6931471805599453f : -INFINITY;
+                        a.lse[(int64_t)row * a.Hq + h] = kv_lse(ctop, csum);
                 }
             }
             __syncthreads();
@@ -280,8 +280,8 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvPages c, KvAttn a, int s
     if (c.starts && (row < c.starts[0] || row >= c.starts[c.B])) return;
     const float m = lane < splits ? ms[0] : -INFINITY;
     const float top = wave_max(m);
-    const float f = m > -INFINITY ? __builtin_amdgcn_exp2f(m - top) : 0.f;
-    const float sum = group_sum<64>(f * ms[1]), share = sum > 0.f ? f * ms[1] / sum : 0.f;
+    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+    const float sum = group_sum<64>(f * ms[1]), share = sum == 0.f ? 0.f : f * ms[1] / sum;
     f32v4_t y = {0.f, 0.f, 0.f, 0.f};
     for (int base = 0; base < splits; base += SIDE * kAhead) {
         if (base) load(base);
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvPages c, KvAttn a, int s
         const float r[4] = {y[0], y[1], y[2], y[3]};
         store_run<4>(static_cast<TO*>(a.out) + row * a.out_row + h * a.out_head + e0, r);
     }
-    if (a.lse && lane == 0) a.lse[v] = sum > 0.f ? (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f : -INFINITY;
+    if (a.lse && lane == 0) a.lse[v] = kv_lse(top, sum);
 }
 
 // ---------------------------------------------------------------- host side

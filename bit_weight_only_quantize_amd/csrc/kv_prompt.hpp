@@ -268,9 +268,8 @@ __global__ __launch_bounds__(512, 2) void kv_prompt_kernel(KvPages c, KvAttn a, 
             const int col = w0 + 16 * n + l16;
             if (col >= columns) continue;
             const int row = s.first + col / a.group, h = head * a.group + col % a.group;
-            const bool some = sm.thr[n] > -INFINITY;
-            const float top = some ? sm.mx[n] * qc[n] : -INFINITY;
-            const float f = sm.l[n] > 0.f ? 1.f / sm.l[n] : 0.f, inv = 1.f / sm.rv[n];
+            const float top = sm.reference(n, qc[n]);
+            const float f = sm.l[n] == 0.f ? 0.f : 1.f / sm.l[n], inv = 1.f / sm.rv[n];
             if (splits > 1) {
                 float* w = static_cast<float*>(a.work) +
                            (((int64_t)row * a.Hq + h) * splits + split) * kv_partial_floats(D);
@@ -291,8 +290,7 @@ __global__ __launch_bounds__(512, 2) void kv_prompt_kernel(KvPages c, KvAttn a, 
                 store_run<NO>(static_cast<TO*>(a.out) + row * a.out_row + h * a.out_head + (4 * g + r) * NO, y);
             }
             if (a.lse && g == 0)
-                a.lse[(int64_t)row * a.Hq + h] =
-                    sm.l[n] > 0.f ? (top + __builtin_amdgcn_logf(sm.l[n])) * 0.6931471805599453f : -INFINITY;
+                a.lse[(int64_t)row * a.Hq + h] = kv_lse(top, sm.l[n]);
         }
     }
 }

@@ -469,6 +469,12 @@ template <int NC, int PIECES, int NO> struct KvSoftmax {
             }
     }
 
+    // The exponent of 2 that a column's weights are relative to; -inf: nothing seen, NaN: no score but NaN.
+    // (After total: a NaN score does not move the reference, and shows in the sum.)
+    __device__ __forceinline__ float reference(int n, float c) const {
+        return thr[n] > -INFINITY ? mx[n] * c : l[n] == 0.f ? -INFINITY : l[n];
+    }
+
     // the whole sum of a column, on its four lanes
     __device__ __forceinline__ void total() {
 #pragma unroll
@@ -478,6 +484,12 @@ template <int NC, int PIECES, int NO> struct KvSoftmax {
         }
     }
 };
+
+// log sum exp from the reference (an exponent of 2) and the sum relative to it; a sum of 0: nothing
+// seen. NaN stays NaN.
+__device__ __forceinline__ float kv_lse(float top, float sum) {
+    return sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
+}
 
 // The keys a tile of columns walks over: the sinks' tiles, then the window's.
 struct KvWalk {

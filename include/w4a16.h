@@ -545,8 +545,9 @@ int w4_kv_read(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows
  * positions and the first `sinks` ones. With z_t = scale * sum_i q[i] k[t][i]
  * over those,
  *   out = sum_t exp(z_t) v[t] / sum_t exp(z_t),   lse = log sum_t exp(z_t);
- * a row that sees nothing gets out = 0 and lse = -infinity. The rows' own keys
- * and values are read from the cache: write them first.
+ * a row that sees nothing gets out = 0 and lse = -infinity, one with a NaN among
+ * its scores NaN in both. The rows' own keys and values are read from the cache:
+ * write them first.
  * q [rows][Hq][D] and out [rows][Hq][D], each fp32 or bf16 on its own; Hq a
  * multiple of Hkv; lse fp32 [rows][Hq] contiguous, or NULL; window, sinks >= 0
  * (sinks without a window change nothing); scale finite, |scale * q| and the keys

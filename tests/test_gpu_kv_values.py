@@ -180,3 +180,46 @@ def test_sums_of_large_and_small_values_of_one_sign(shape, power):
     b = s.batch(max_rows=max(s.n), max_len=shape["max_len"])
     got, lse = w4.kv_attention(torch.from_numpy(q).cuda(), s.cache(), b, want_lse=True)
     check_rows(s, q, got, lse, "f32", "f32", terms=1, rows=[0, s.rows // 2, s.rows - 1])
+
+
+# ---------------------------------------------------------------- NaN
+@pytest.mark.parametrize("D,types", [(64, ("f32", "f32")), (128, ("bf16", "bf16")), (256, ("bf16", "f32"))])
+@pytest.mark.parametrize("shape", [SPLIT, PARTS, PROMPT, PROMPT_PARTS], ids=["split", "parts", "prompt", "prompt in parts"])
+def test_nan_shows_in_out_and_lse(shape, D, types):
+    """A query with a NaN, an infinite one, a key or value of NaN scale: NaN in the rows that have or see
+    it, in lse as well (-infinity means a row that sees nothing), and the bits of all others unchanged."""
+    s, q = make(shape, D, f"nan.{D}", types[0])
+    want, wl = attend(s, s.cache(), q, *types)
+    bad = q.copy()
+    last = s.rows - 1
+    bad[0, 0, 3], bad[0, 1], bad[last, -1, D - 1] = NAN, NAN, INF
+    hit = np.zeros(q.shape[:2], dtype=bool)
+    hit[0, 0] = hit[0, 1] = hit[last, -1] = True
+    got, lse = attend(s, s.cache(), bad, *types)
+    h = torch.from_numpy(hit).cuda()
+    assert torch.isnan(got[h]).all() and torch.isnan(lse[h]).all()
+    assert same_bits(got[~h], want[~h]) and same_bits(lse[~h], wl[~h])
+    # keys and values: the second last row of the first sequence and what follows see them
+    n, L = s.n[0], s.lens[0]
+    p, o = (int(x) for x in s.place(0, L - 2))
+    sees = np.arange(s.rows)
+    sees = torch.from_numpy((sees >= n - 2) & (sees < n)).cuda()
+    for half in "kv":
+        cache = s.cache()
+        (cache.k_scales if half == "k" else cache.v_scales)[p, 0, o] = NAN
+        got, lse = attend(s, cache, q, *types)
+        G = shape["G"]
+        assert torch.isnan(got[sees][:, :G]).all()
+        assert torch.isnan(lse[sees][:, :G]).all() if half == "k" else same_bits(lse, wl)
+        assert same_bits(got[~sees], want[~sees]) and same_bits(lse[~sees], wl[~sees])
+        assert same_bits(got[sees][:, G:], want[sees][:, G:]) and same_bits(lse[sees][:, G:], wl[sees][:, G:])
+
+
+def test_all_scores_nan():
+    """Every key of NaN scale: NaN, not the result of a row that sees nothing."""
+    for shape in (SPLIT, PARTS, PROMPT, PROMPT_PARTS):
+        s, q = make(shape, 64, "allnan")
+        cache = s.cache()
+        cache.k_scales.fill_(NAN)
+        got, lse = attend(s, cache, q, "f32", "f32")
+        assert torch.isnan(got).all() and torch.isnan(lse).all()
