@@ -201,10 +201,11 @@ template <bool EXACT> struct KvScaling {
         sign = some ? copysignf(1.f, scale) : 0.f;
     }
     static __device__ __forceinline__ float zero(float sum) { return EXACT ? 0.f : -8.f * 0x1p-24f * sum; }
-    // finite and positive for any finite scale and query
+    // Finite and positive for any finite scale and query. Down to the least subnormal: scores times key
+    // scales reach 2^123, and what c loses under 2^-126 is less than 2^-26 of the exponent even so.
     __device__ __forceinline__ float c(float scale) const {
         if (sign == 0.f) return 1.f;
-        return fminf(fmaxf(ldexpf(fabsf(scale) * 1.4426950408889634f, (EXACT ? 0 : 24) - e), 0x1p-120f), 0x1p120f);
+        return fminf(fmaxf(ldexpf(fabsf(scale), (EXACT ? 0 : 24) - e) * 1.4426950408889634f, 0x1p-149f), 0x1p120f);
     }
     // one operand (and its share of sum x) from eight elements
     template <int PIECES>

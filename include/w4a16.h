@@ -551,7 +551,7 @@ int w4_kv_read(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows
  * q [rows][Hq][D] and out [rows][Hq][D], each fp32 or bf16 on its own; Hq a
  * multiple of Hkv; lse fp32 [rows][Hq] contiguous, or NULL; window, sinks >= 0
  * (sinks without a window change nothing); scale finite, |scale * q| and the keys
- * under 2^100. out must not overlap q or the cache. workspace: device
+ * under 2^100, scores under 2^120. out must not overlap q or the cache. workspace: device
  * memory of at least w4_kv_attention_workspace_bytes(...) bytes for the same
  * cache, batch (its host values), Hq, window and sinks (W4_EWORKSPACE
  * otherwise; may be NULL when that is 0); its contents on entry do not matter,

@@ -223,3 +223,17 @@ def test_all_scores_nan():
         cache.k_scales.fill_(NAN)
         got, lse = attend(s, cache, q, "f32", "f32")
         assert torch.isnan(got).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("shape", [SPLIT, PROMPT], ids=["split", "prompt"])
+@pytest.mark.parametrize("qp,kp,scale", [(-140, 94, 1.0), (-30, 94, 2.0 ** -100), (-109, 94, 1.0), (-149, 0, 1.0),
+                                         (-120, 90, 2.0 ** 30), (124, 14, 2.0 ** -140)])
+def test_small_queries_against_large_keys(shape, qp, kp, scale):
+    """Queries and scales far under 1 against keys near 2^100, a subnormal scale: scores far from both ends."""
+    s, q = make(shape, 64, "tiny")
+    q = (np.sign(q) * np.exp2(np.float64(qp)) * np.ceil(np.abs(q))).astype(np.float32)
+    for b in range(s.B):
+        s.quant[0][b] = oracle.kv_quantize((s.x[0][b] * np.float32(2.0 ** kp)).astype(np.float32))
+        s.deq[0][b] = oracle.kv_dequant(*s.quant[0][b])
+    got, lse = attend(s, s.cache(), q, "f32", "f32", scale=scale)
+    check_rows(s, q, got, lse, "f32", "f32", scale=scale, rows=[0, 3, s.rows - 1])
