@@ -86,11 +86,18 @@ template <int E> __device__ __forceinline__ void store_run(float* p, const float
         for (int i = 0; i < E; ++i) p[i] = v[i];
     }
 }
+// Two values to bf16, to nearest even by v_cvt_pk_bf16_f32: a NaN stays one whatever its mantissa
+// (rounding by an integer addition would carry a mantissa of ones into the exponent and sign).
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    typedef float f2_t __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2_t __attribute__((ext_vector_type(2)));
+    const f2_t f = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, b2_t));
+}
 template <int E> __device__ __forceinline__ void store_run(__bf16* p, const float* v) {
     uint32_t w[(E + 1) / 2];
 #pragma unroll
-    for (int i = 0; i < (E + 1) / 2; ++i)
-        w[i] = f32_to_bf16_rne(v[2 * i]) | (2 * i + 1 < E ? f32_to_bf16_rne(v[2 * i + 1]) << 16 : 0u);
+    for (int i = 0; i < (E + 1) / 2; ++i) w[i] = bf16_pair(v[2 * i], 2 * i + 1 < E ? v[2 * i + 1] : 0.f);
     if constexpr (E % 8 == 0) {
 #pragma unroll
         for (int i = 0; i < E / 2; i += 4)

@@ -237,3 +237,33 @@ def test_small_queries_against_large_keys(shape, qp, kp, scale):
         s.deq[0][b] = oracle.kv_dequant(*s.quant[0][b])
     got, lse = attend(s, s.cache(), q, "f32", "f32", scale=scale)
     check_rows(s, q, got, lse, "f32", "f32", scale=scale, rows=[0, 3, s.rows - 1])
+
+
+def test_nan_of_any_payload_stays_nan_in_bf16():
+    """A NaN whose mantissa is all ones must not carry into the sign: read back and attended, rows are NaN."""
+    s, q = make(SPLIT, 64, "payload")
+    cache = s.cache()
+    for bits in (0x7FFFFFFF, 0x7F800001, -1, 0x7FC00000):
+        for t in (cache.k_scales, cache.v_scales):
+            t.view(torch.int32).fill_(bits)
+        for x in w4.kv_read(cache, s.batch(), dtype=torch.bfloat16):
+            assert torch.isnan(x).all()
+        assert torch.isnan(attend(s, cache, q, "f32", "bf16")[0]).all()
+
+
+def test_rounding_to_bf16():
+    """Values on, next to and between two bf16 values, subnormals and the ends of the type: to nearest, ties to
+    even, bit for bit as the conversion of the fp32 value."""
+    rng = np.random.default_rng(11)
+    bits = rng.integers(0, 0x7F80, 4096).astype(np.uint32) << 16
+    bits += np.array([0, 1, 0x7FFF, 0x8000, 0x8001, 0xFFFF], dtype=np.uint32)[rng.integers(0, 6, 4096)]
+    bits[:8] = [0, 1, 0x8000, 0x8001, 0x00800000, 0x7F7FFFFF, 0x7F7F8000, 0x7F7F7FFF]
+    cache = w4.kv_pages(1, 1, 4096, 64)
+    cache.k_codes.fill_(0x79)                                  # codes 1 and -1: the scale itself, both signs
+    cache.k_scales.copy_(torch.from_numpy(bits.view(np.float32)).view(1, 1, 4096))
+    b = w4.KVBatch(torch.tensor([4096], dtype=torch.int32, device="cuda"), rows=4096)
+    k = torch.empty((4096, 1, 64), dtype=torch.bfloat16, device="cuda")
+    w4.kv_read(cache, b, k=k)
+    want = torch.from_numpy(bits.view(np.float32)).bfloat16()
+    assert torch.equal(k[:, 0, 0].cpu().view(torch.int16), want.view(torch.int16))
+    assert torch.equal(k[:, 0, 63].cpu().view(torch.int16), (-want).view(torch.int16))
