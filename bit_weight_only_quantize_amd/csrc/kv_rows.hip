@@ -100,9 +100,9 @@ __global__ __launch_bounds__(256) void kv_rows_kernel(KvPages c, KvRowsArg a, Kv
 #pragma unroll
                 for (int k = 0; k < AHEAD; ++k) {
                     if (h + k * step >= h1) break;
-                    float m = 0.f;
+                    float m = fabsf(e[k][0]);  // fmaxf passes over NaN: a vector of nothing else has a NaN scale
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(e[k][j]));
+                    for (int j = 1; j < 8; ++j) m = fmaxf(m, fabsf(e[k][j]));
                     m = lanes_max<LANES>(m);
                     const float sc = m / 7.5f;
                     const uint32_t w = kv_codes(e[k], sc);

@@ -267,3 +267,36 @@ def test_rounding_to_bf16():
     want = torch.from_numpy(bits.view(np.float32)).bfloat16()
     assert torch.equal(k[:, 0, 0].cpu().view(torch.int16), want.view(torch.int16))
     assert torch.equal(k[:, 0, 63].cpu().view(torch.int16), (-want).view(torch.int16))
+
+
+# ---------------------------------------------------------------- writing what is not finite
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_write_of_infinities_and_nan_equals_the_single_sequence_codec(dtype):
+    """Infinities and NaN among the values: the same codes and scales as w4_kv_quantize's, bit for bit."""
+    x = values((40, 3, 128), "wnan", dtype)
+    x[0, 0, 5], x[1, 1, 127], x[2, :, 0], x[3, 2] = INF, -INF, NAN, NAN
+    x[4, 0, :2], x[5, 0, :3], x[6, 1] = [INF, -INF], [NAN, INF, -INF], INF
+    x[7, 2] = 0
+    x[7, 2, 9] = NAN
+    xd = to_dev(x, dtype)
+    codes, scales = w4.kv_cache(3, 40)
+    w4.kv_quantize(xd.float(), codes, scales, 0)
+    cache = w4.kv_pages(1, 3, 40)
+    w4.kv_write(xd, xd, cache, w4.KVBatch(torch.tensor([40], dtype=torch.int32, device="cuda"), rows=40))
+    for c, t in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)):
+        assert torch.equal(t[0].view(torch.int32), scales.view(torch.int32))
+        assert torch.equal(c[0], codes)
+
+
+def test_infinite_values_of_later_rows_end_to_end():
+    """An overflowed row written into the cache: the rows before it are those of a cache without it."""
+    s, q = make(SPLIT, 128, "overflow", "bf16")
+    k, v = (to_dev(s.new_rows(i), "bf16") for i in (0, 1))
+    cache, b = s.cache(upto=[38, 39]), s.batch()
+    w4.kv_write(k, v, cache, b)
+    want = w4.kv_attention(to_dev(q, "bf16"), cache, b)
+    v[6, 0, 17], k[6, 1, 3] = INF, INF
+    w4.kv_write(k, v, cache, b)
+    got = w4.kv_attention(to_dev(q, "bf16"), cache, b)
+    assert same_bits(got[:6], want[:6]) and same_bits(got[12:], want[12:])
+    assert not torch.isfinite(got[6:12]).all()
