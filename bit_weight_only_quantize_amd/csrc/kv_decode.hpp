@@ -263,51 +263,53 @@ template <int D, typename TO>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvPages c, KvAttn a, int splits) {
     constexpr int PF = kv_partial_floats(D), LANES = D / 4, SIDE = 64 / LANES, kAhead = 8;
     const int lane = threadIdx.x & 63;
-    const int64_t v = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (v >= (int64_t)c.rows * a.Hq) return;  // whole wavefront
-    const int row = (int)(v / a.Hq), h = (int)(v - (int64_t)row * a.Hq);
-    const float* w = static_cast<const float*>(a.work) + v * splits * PF;
-    const int mine = min(lane, splits - 1), side = lane / LANES, e0 = 4 * (lane % LANES);
-    const f32v2_t ms = *reinterpret_cast<const f32v2_t*>(w + (int64_t)mine * PF + D);
-    f32v4_t x[kAhead];
-    auto load = [&](int base) {
+    const int64_t vectors = (int64_t)c.rows * a.Hq;
+    for (int64_t v = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); v < vectors; v += (int64_t)gridDim.x * 4) {  // whole wavefronts
+        const int row = (int)(v / a.Hq), h = (int)(v - (int64_t)row * a.Hq);
+        const float* w = static_cast<const float*>(a.work) + v * splits * PF;
+        const int mine = min(lane, splits - 1), side = lane / LANES, e0 = 4 * (lane % LANES);
+        const f32v2_t ms = *reinterpret_cast<const f32v2_t*>(w + (int64_t)mine * PF + D);
+        f32v4_t x[kAhead];
+        auto load = [&](int base) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            x[k] = *reinterpret_cast<const f32v4_t*>(w + (int64_t)min(base + SIDE * k + side, splits - 1) * PF + e0);
-    };
-    load(0);
-    // rows of no sequence have no parts
-    if (c.starts && (row < c.starts[0] || row >= c.starts[c.B])) return;
-    const float m = lane < splits ? ms[0] : -INFINITY;
-    const float top = wave_max(m);
-    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
-    const float sum = group_sum<64>(f * ms[1]), share = sum == 0.f ? 0.f : f * ms[1] / sum;
-    f32v4_t y = {0.f, 0.f, 0.f, 0.f};
-    for (int base = 0; base < splits; base += SIDE * kAhead) {
-        if (base) load(base);
+            for (int k = 0; k < kAhead; ++k)
+                x[k] = *reinterpret_cast<const f32v4_t*>(w + (int64_t)min(base + SIDE * k + side, splits - 1) * PF + e0);
+        };
+        load(0);
+        // rows of no sequence have no parts
+        if (c.starts && (row < c.starts[0] || row >= c.starts[c.B])) continue;
+        const float m = lane < splits ? ms[0] : -INFINITY;
+        const float top = wave_max(m);
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+        const float sum = group_sum<64>(f * ms[1]), share = sum == 0.f ? 0.f : f * ms[1] / sum;
+        f32v4_t y = {0.f, 0.f, 0.f, 0.f};
+        for (int base = 0; base < splits; base += SIDE * kAhead) {
+            if (base) load(base);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int i = base + SIDE * k + side;
-            const float fi = __shfl(share, min(i, 63));
-            y += x[k] * (i < splits ? fi : 0.f);
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = base + SIDE * k + side;
+                const float fi = __shfl(share, min(i, 63));
+                y += x[k] * (i < splits ? fi : 0.f);
+            }
         }
-    }
 #pragma unroll
-    for (int o = LANES; o < 64; o <<= 1)
+        for (int o = LANES; o < 64; o <<= 1)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] += __shfl_xor(y[e], o);
-    if (side == 0) {
-        const float r[4] = {y[0], y[1], y[2], y[3]};
-        store_run<4>(static_cast<TO*>(a.out) + row * a.out_row + h * a.out_head + e0, r);
+            for (int e = 0; e < 4; ++e) y[e] += __shfl_xor(y[e], o);
+        if (side == 0) {
+            const float r[4] = {y[0], y[1], y[2], y[3]};
+            store_run<4>(static_cast<TO*>(a.out) + row * a.out_row + h * a.out_head + e0, r);
+        }
+        if (a.lse && lane == 0) a.lse[v] = kv_lse(top, sum);
     }
-    if (a.lse && lane == 0) a.lse[v] = kv_lse(top, sum);
 }
 
 // ---------------------------------------------------------------- host side
 template <int D, typename TO>
 hipError_t launch_kv_join(const KvPages& c, const KvAttn& a, int splits, hipStream_t st) {
-    hipLaunchKernelGGL((kv_join_kernel<D, TO>), dim3((unsigned)(((int64_t)c.rows * a.Hq + 3) / 4)), dim3(256), 0, st,
-                       c, a, splits);
+    const int64_t blocks = ((int64_t)c.rows * a.Hq + 3) / 4;  // a launch holds 2^32 - 1 threads: more loop
+    hipLaunchKernelGGL((kv_join_kernel<D, TO>), dim3((unsigned)(blocks < (1 << 22) ? blocks : 1 << 22)), dim3(256), 0,
+                       st, c, a, splits);
     return hipGetLastError();
 }
 

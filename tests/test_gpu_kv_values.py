@@ -300,3 +300,26 @@ def test_infinite_values_of_later_rows_end_to_end():
     got = w4.kv_attention(to_dev(q, "bf16"), cache, b)
     assert same_bits(got[:6], want[:6]) and same_bits(got[12:], want[12:])
     assert not torch.isfinite(got[6:12]).all()
+
+
+# ---------------------------------------------------------------- sizes
+def test_parts_of_more_rows_than_one_grid_holds():
+    """2^26 (row, query head) pairs whose keys are taken in parts: one wavefront each would pass the most
+    threads of a launch. One sequence of one row; the other rows belong to none and stay as they are."""
+    rows, Hq = 1 << 20, 64
+    s = Batch([512], [1], 1, 64, 16, "grid")
+    cache = s.cache()
+    lens = torch.tensor([512], dtype=torch.int32, device="cuda")
+    b = w4.KVBatch(lens, table=torch.from_numpy(s.table).cuda(), rows=rows, max_rows=1, max_len=512,
+                   starts=torch.tensor([rows - 1, rows], dtype=torch.int32, device="cuda"))
+    assert w4.kv_attention_workspace(cache, b, Hq).numel() > 0
+    q = torch.empty((1, Hq, 64), dtype=torch.bfloat16, device="cuda").expand(rows, Hq, 64)
+    x = values((1, Hq, 64), "grid.q", "bf16")
+    q[-1:].copy_(to_dev(x, "bf16"))                            # one row of queries for all
+    out = torch.full((rows, Hq, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((rows, Hq), 3.0, dtype=torch.float32, device="cuda")
+    w4.kv_attention(q, cache, b, out=out, lse=lse)
+    check_rows(s, x, out[-1:], lse[-1:], "bf16", "bf16")
+    assert (out[:-1] == 3.0).all() and (lse[:-1] == 3.0).all()
+    del q, out, lse
+    torch.cuda.empty_cache()                                   # the workspace alone took 73 GB
