@@ -763,6 +763,8 @@ int w4_kv_weighted_sum_append(const float* p, const float* v_new, int64_t n, int
 
 // ---------------------------------------------------------------- batched INT4 KV cache
 static const int64_t kInt31 = 0x7fffffffLL;
+// rows times heads: kernels count on in steps of up to 512 from the last of them
+static const int64_t kMostVectors = kInt31 - 4095;
 
 // Checks the pool and the batch and gives the kernels' view of them. B == 0 and
 // rows == 0 leave *v unset: the caller returns at once.
@@ -776,7 +778,7 @@ static int kv_check_pages(const w4_kv_pages* c, const w4_kv_batch* b, w4::KvPage
         return fail(W4_ESHAPE, "num_pages=%lld Hkv=%lld page_size=%lld out of range",
                     (long long)c->num_pages, (long long)c->Hkv, (long long)c->page_size);
     if (b->B < 0 || b->rows < 0 || b->max_rows < 0 || b->max_len < 0 || b->B > (1 << 20) ||
-        b->rows > kInt31 / c->Hkv)
+        b->rows > kMostVectors / c->Hkv)
         return fail(W4_ESHAPE, "B=%lld rows=%lld max_rows=%lld max_len=%lld out of range",
                     (long long)b->B, (long long)b->rows, (long long)b->max_rows, (long long)b->max_len);
     if (b->B == 0 || b->rows == 0) return W4_OK;
@@ -906,8 +908,8 @@ int w4_kv_read(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows
 // Query heads and mask; the sizes of the launch
 static int kv_check_heads(const w4_kv_pages* c, const w4_kv_batch* b, int64_t Hq, int64_t window,
                           int64_t sinks) {
-    if (Hq < 1 || Hq % c->Hkv || Hq > kInt31 / (b->rows > 0 ? b->rows : 1))
-        return fail(W4_ESHAPE, "Hq=%lld must be a positive multiple of Hkv=%lld, with rows * Hq in 31 bits",
+    if (Hq < 1 || Hq % c->Hkv || Hq > kMostVectors / (b->rows > 0 ? b->rows : 1))
+        return fail(W4_ESHAPE, "Hq=%lld must be a positive multiple of Hkv=%lld, with rows * Hq <= 2^31 - 4096",
                     (long long)Hq, (long long)c->Hkv);
     if (window < 0 || sinks < 0)
         return fail(W4_ESHAPE, "window=%lld sinks=%lld out of range", (long long)window, (long long)sinks);

@@ -474,9 +474,10 @@ int w4_kv_weighted_sum_append(const float* p, const float* v_new, int64_t n, int
  *     holds its positions j * page_size and up (j < table_width <=
  *     table_stride); page_size is then a power of two, 16 or more. NULL:
  *     sequence b owns page b (num_pages >= B) and page_size is any size.
- *   rows: rows of the packed tensors, at most. max_rows: the most rows of one
- *     sequence, and max_len: the largest of lens; both only shape the launch
- *     (speed, not results), 0 if unknown.
+ *   rows: rows of the packed tensors, at most; rows times the heads of a row
+ *     tensor <= 2^31 - 4096. max_rows: the most rows of one sequence, and max_len:
+ *     the largest of lens; both only shape the launch (speed, not results), 0 if
+ *     unknown.
  * Contents are not trusted with memory: a page outside [0, num_pages) holds no
  * position (nothing is written to it, it reads back as zeros, attention does
  * not see it), lens are clamped to [0, capacity] and starts to [0, rows], and a
