@@ -193,9 +193,8 @@ __global__ __launch_bounds__(512, 2) void kv_prompt_kernel(KvPages c, KvAttn a, 
             fetch(i0 + TILES);
             const KvStage<D>& st = stage[buf];
             const int count = min(TILES, tiles - i0);
-            // a stage that all of this wavefront's columns see whole, or tile by tile
-            const int first = walk.tile(j0 + i0) * 32, last = walk.tile(j0 + i0 + count - 1) * 32;
-            const bool pages = __builtin_amdgcn_ballot_w64(lane < 2 * TILES && (&st.n[0][0])[lane] != 16) == 0;
+            // no key of its tiles is missing (pages that are not there, the end of the pool)
+            const bool pages = __builtin_amdgcn_ballot_w64(lane < 2 * count && (&st.n[0][0])[lane] != 16) == 0;
 #pragma unroll 1
             for (int ti = 0; ti < TILES; ++ti) {
                 if (ti >= count) continue;
