@@ -617,7 +617,7 @@ def kv_attention(q: torch.Tensor, cache: KVPages, batch: KVBatch, scale: Optiona
     """Causal attention of the batch's rows q (fp32 or bf16 [rows][Hq][D], strided) over their sequences'
     cached positions, with window > 0 over the last `window` and the first `sinks` ones only. scale:
     1 / sqrt(D) by default. Returns out (q's type unless given), or (out, lse) with lse fp32 [rows][Hq]
-    when lse is given or want_lse. Rows of no sequence are left as they are; a row that sees nothing gets
+    (contiguous, 16-byte aligned) when lse is given or want_lse. Rows of no sequence are left as they are; a row that sees nothing gets
     0 and -inf. workspace: kv_attention_workspace(...)'s (allocated for the call by default); calls that
     may overlap need their own."""
     Hq = q.shape[1] if q.dim() == 3 else 0
@@ -632,6 +632,8 @@ def kv_attention(q: torch.Tensor, cache: KVPages, batch: KVBatch, scale: Optiona
                 or lse.get_device() != cache.index:
             raise ValueError(f"lse must be float32 [{batch.rows} or more][{Hq}] on the cache's device")
         plse = lse.data_ptr()
+        if plse % 16:
+            raise ValueError("lse must be 16-byte aligned (a slice of a larger tensor may not be)")
     elif want_lse:
         lse = out.new_empty((q.shape[0], Hq), dtype=torch.float32)
         plse = lse.data_ptr()

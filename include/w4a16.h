@@ -550,13 +550,14 @@ int w4_kv_read(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows
  * its scores NaN in both. The rows' own keys and values are read from the cache:
  * write them first.
  * q [rows][Hq][D] and out [rows][Hq][D], each fp32 or bf16 on its own; Hq a
- * multiple of Hkv; lse fp32 [rows][Hq] contiguous, or NULL; window, sinks >= 0
- * (sinks without a window change nothing); scale finite, |scale * q| and the keys
- * under 2^100, scores under 2^120. out must not overlap q or the cache. workspace: device
- * memory of at least w4_kv_attention_workspace_bytes(...) bytes for the same
- * cache, batch (its host values), Hq, window and sinks (W4_EWORKSPACE
- * otherwise; may be NULL when that is 0); its contents on entry do not matter,
- * on return they are unspecified. Calls sharing a workspace must not overlap.
+ * multiple of Hkv; lse fp32 [rows][Hq] contiguous and 16-byte aligned, or NULL;
+ * window, sinks >= 0 (sinks without a window change nothing); scale finite,
+ * |scale * q| and the keys under 2^100, scores under 2^120. out must not overlap q
+ * or the cache. workspace: device memory of at least
+ * w4_kv_attention_workspace_bytes(...) bytes for the same cache, batch (its host
+ * values), Hq, window and sinks (W4_EWORKSPACE otherwise; may be NULL when that is
+ * 0); its contents on entry do not matter, on return they are unspecified. Calls
+ * sharing a workspace must not overlap.
  * A row's result depends on nothing but what the row sees: keys and values hidden
  * from it may be of any size, infinite or NaN. Among those it sees, a weight times
  * value scale under 2^-33 of the row's largest is dropped.

@@ -323,3 +323,17 @@ def test_parts_of_more_rows_than_one_grid_holds():
     assert (out[:-1] == 3.0).all() and (lse[:-1] == 3.0).all()
     del q, out, lse
     torch.cuda.empty_cache()                                   # the workspace alone took 73 GB
+
+
+# ---------------------------------------------------------------- refusals of the binding
+def test_lse_that_is_not_16_byte_aligned_is_refused():
+    """A slice of a larger tensor is taken where it begins on 16 bytes, and refused before the launch elsewhere."""
+    s, q = make(dict(lens=[20], rows=[2], Hkv=1, G=5, page=16), 64, "align")
+    cache, b, qd = s.cache(), s.batch(), torch.from_numpy(q).cuda()
+    want = w4.kv_attention(qd, cache, b, want_lse=True)[1]
+    hold = torch.full((8, 5), 2.0, device="cuda")
+    with pytest.raises(ValueError, match="aligned"):
+        w4.kv_attention(qd, cache, b, lse=hold[1:3])
+    assert (hold == 2.0).all()
+    w4.kv_attention(qd, cache, b, lse=hold[4:6])
+    assert same_bits(hold[4:6], want) and (hold[:4] == 2.0).all() and (hold[6:] == 2.0).all()
