@@ -603,10 +603,18 @@ def kv_read(cache: KVPages, batch: KVBatch, dtype: torch.dtype = torch.bfloat16,
     return k, v
 
 
+def _span(v: int, name: str) -> int:
+    """A window or number of sinks for a 64-bit argument: anything past every position is alike."""
+    if v < 0:
+        raise ValueError(f"{name} must not be negative")
+    return min(v, 1 << 62)
+
+
 def kv_attention_workspace(cache: KVPages, batch: KVBatch, Hq: int, window: int = 0,
                            sinks: int = 0) -> torch.Tensor:
     """A workspace for kv_attention with these sizes (empty where it needs none)."""
-    n = int(lib().w4_kv_attention_workspace_bytes(cache._ref, batch._ref, Hq, window, sinks))
+    n = int(lib().w4_kv_attention_workspace_bytes(cache._ref, batch._ref, Hq, _span(window, "window"),
+                                                  _span(sinks, "sinks")))
     return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
@@ -620,6 +628,7 @@ def kv_attention(q: torch.Tensor, cache: KVPages, batch: KVBatch, scale: Optiona
     (contiguous, 16-byte aligned) when lse is given or want_lse. Rows of no sequence are left as they are; a row that sees nothing gets
     0 and -inf. workspace: kv_attention_workspace(...)'s (allocated for the call by default); calls that
     may overlap need their own."""
+    window, sinks = _span(window, "window"), _span(sinks, "sinks")
     Hq = q.shape[1] if q.dim() == 3 else 0
     dq = _rows_desc(q, "q", cache, batch, Hq)
     if out is None:

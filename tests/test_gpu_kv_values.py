@@ -337,3 +337,20 @@ def test_lse_that_is_not_16_byte_aligned_is_refused():
     assert (hold == 2.0).all()
     w4.kv_attention(qd, cache, b, lse=hold[4:6])
     assert same_bits(hold[4:6], want) and (hold[:4] == 2.0).all() and (hold[6:] == 2.0).all()
+
+
+def test_windows_past_64_bits():
+    """A window or sinks past any position, however large a Python number: all positions; negative ones are refused."""
+    s, q = make(dict(lens=[70], rows=[3], Hkv=1, G=5, page=16), 64, "span")
+    cache, b, qd = s.cache(), s.batch(), torch.from_numpy(q).cuda()
+    want = w4.kv_attention(qd, cache, b)
+    for big in (2 ** 63 - 1, 2 ** 63, 2 ** 64 + 5):
+        assert same_bits(w4.kv_attention(qd, cache, b, window=big), want)
+        assert same_bits(w4.kv_attention(qd, cache, b, window=3, sinks=big), want)
+        assert w4.kv_attention_workspace(cache, b, 5, window=3, sinks=big).numel() == \
+            w4.kv_attention_workspace(cache, b, 5).numel()
+    for bad in (-1, -2 ** 64 + 5):
+        with pytest.raises(ValueError, match="negative"):
+            w4.kv_attention(qd, cache, b, window=bad)
+        with pytest.raises(ValueError, match="negative"):
+            w4.kv_attention(qd, cache, b, window=3, sinks=bad)
