@@ -354,3 +354,15 @@ def test_windows_past_64_bits():
             w4.kv_attention(qd, cache, b, window=bad)
         with pytest.raises(ValueError, match="negative"):
             w4.kv_attention(qd, cache, b, window=3, sinks=bad)
+
+
+# ---------------------------------------------------------------- repeated calls
+@pytest.mark.parametrize("types", [("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("shape", [PARTS, PROMPT], ids=["parts", "prompt"])
+def test_repeated_calls_of_mixed_types_give_the_same_bits(shape, types):
+    s, q = make(shape, 128, "again", types[0])
+    cache = s.cache()
+    first = attend(s, cache, q, *types)
+    for _ in range(3):
+        for x, y in zip(attend(s, cache, q, *types), first):
+            assert same_bits(x, y)
