@@ -26,13 +26,21 @@ template <int D> hipError_t launch(const KvPages& c, const KvAttn& a, bool q_bf1
 // (and no shorter than the longest workgroup) plus what a workgroup costs besides, two
 // tiles' time, in kv_prompt_kernel 14 (its first stage and last barriers serve few tiles);
 // parts cost two more for the launch that joins them. A tile takes a wavefront about 4850
-// clocks in kv_split_kernel (5900 with D = 256; 6000 in two pieces) and 3500 (5400) in
+// clocks in kv_split_kernel (5900 with D = 256; 6000 in two pieces) and 3500 (4600) in
 // kv_prompt_kernel, for the same columns. Measured, 8 kv heads, bf16, us:
 //   split kernel, a batch of 48 of up to 8192 positions: 79 whole, 51 in two parts (one
 //   round), 55 in eight, 69 in sixteen; two of up to 131072: 50 in 48 parts, 67 in 16.
-//   split against prompt kernel (G = 4 unless given): 512 rows 18 / 36, 2048 rows 110 / 104
-//   (D = 256: 197 / 130), 64 rows behind 16384 49 / 55, 512 behind 16384 231 / 202,
-//   8192 rows of 32 heads with G = 1 1030 / 743.
+//   split against prompt kernel, each in the parts that the estimate gives it (G = 4; the last with
+//   G = 1, 32 kv heads, 16 with D = 256):
+//                  512 rows   2048 rows   64 behind 16384   512 behind 16384   8192 rows
+//     bf16  D 128   18 / 37    98 / 121       47 / 54           244 / 211       969 / 728
+//           D 256   26 / 41   180 / 128       82 / 80           492 / 393      1031 / 800
+//     fp32  D 128   21 / 43   126 / 146       60 / 67           358 / 285      1365 / 1000
+//           D 256   34 / 46   248 / 174      117 / 97           742 / 517      1541 / 1040
+// The estimate takes the faster one of each pair, but for fp32, D = 256, 64 behind 16384.
+// It takes `rows` for every sequence's where the caller gives no max_rows: 64 single tokens with
+// starts, up to 8192 positions, take 73 us with the bounds and 388 without. One kernel serves
+// all sequences of a call: 47 such tokens beside 1024 rows behind 7168 take 1003, apart 62 and 199.
 namespace {
 struct KvGuess {
     int64_t clocks;
@@ -74,7 +82,7 @@ KvPlan kv_plan(const KvPages& c, int D, int group, int pieces, int64_t max_rows,
             mean = keys < mean ? keys : mean;
         }
         const int fit = 256 * (prompt ? 1 : p.nc == 1 && D < 256 ? 3 : 2);
-        const int clocks = prompt ? (pieces == 1 ? 3500 : 5400) : pieces == 2 ? 6000 : D == 256 ? 5900 : 4850;
+        const int clocks = prompt ? (pieces == 1 ? 3500 : 4600) : pieces == 2 ? 6000 : D == 256 ? 5900 : 4850;
         guess[prompt] = kv_guess(p.column_tiles * pairs, fit, (keys + 31) / 32, (mean + 31) / 32, prompt ? 1 : 4,
                                  prompt ? 14 : 2, clocks);
         p.splits = guess[prompt].splits;
