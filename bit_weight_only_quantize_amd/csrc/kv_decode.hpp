@@ -12,8 +12,8 @@
 //
 // 16 columns cost what one does (the matrix cores' least width), so a kv head's query
 // heads share one pass over its codes: 136 bytes a key of 128 + 128 values. Long contexts
-// are bound by memory: two of up to 131072 positions, 5 query heads a kv head, 43 us for
-// 260 MB (6.0 TB/s, some of it from the last-level cache), a ragged batch of 48 of up to
+// are bound by memory: two of up to 131072 positions, 5 query heads a kv head, 44 us for
+// 260 MB (5.9 TB/s, some of it from the last-level cache), a ragged batch of 48 of up to
 // 8192 48 us for 196 MB; the join 4. A tile takes one of a SIMD's three wavefronts some 3500 clocks: 900 the
 // values' unpacking and product, 760 the weights, 770 finding and asking for the next
 // keys, 170 waiting for them. Short ones are bound by the chain before the first product

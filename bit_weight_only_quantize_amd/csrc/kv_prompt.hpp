@@ -9,11 +9,11 @@
 // every tile for its own columns: unpacking costs an eighth of what it does in
 // kv_split_kernel. The causal edge makes the last columns the longest: they go first.
 //
-// A tile takes each wavefront about 3500 clocks, two wavefronts a SIMD; the matrix
+// A tile takes each wavefront about 3400 clocks, two wavefronts a SIMD; the matrix
 // cores work 30% of the time and the vector unit 60%, with a wavefront's phases waiting
-// on one another (scores 380, softmax 1000 to 1250, second product 390, its share
-// of the filling 500, barriers 200 to 900). 8192 rows of 32 heads of 128: 745 us, 740
-// TFLOP/s over the causal pairs, where a library's bf16 product of 8192^3 runs at 1205.
+// on one another. 8192 rows of 32 heads of 128: 730 us, 753 TFLOP/s over the causal pairs,
+// where a library's bf16 product of 8192^3 runs at 1205; with fp32 rows, in two pieces, 1000
+// (13 to 16 of its vector registers are spilled; no other kernel here spills vector registers).
 #pragma once
 
 #include "kv_decode.hpp"
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(512, 2) void kv_prompt_kernel(KvPages c, KvAttn a, 
 #pragma unroll
                     for (int h = 0; h < 2; ++h) kf[w][h] = st.k[ti][h][w][lane];
                 __builtin_amdgcn_sched_barrier(0);
-                __builtin_amdgcn_s_setprio(1);  // products before the other wavefront's softmax
+                __builtin_amdgcn_s_setprio(1);  // products before the other wavefront's softmax: 735 -> 729 us
                 f32v4_t z[NC][2];
 #pragma unroll
                 for (int n = 0; n < NC; ++n) z[n][0] = z[n][1] = f32v4_t{0.f, 0.f, 0.f, 0.f};

@@ -476,8 +476,10 @@ int w4_kv_weighted_sum_append(const float* p, const float* v_new, int64_t n, int
  *     sequence b owns page b (num_pages >= B) and page_size is any size.
  *   rows: rows of the packed tensors, at most; rows times the heads of a row
  *     tensor <= 2^31 - 4096. max_rows: the most rows of one sequence, and max_len:
- *     the largest of lens; both only shape the launch (speed, not results), 0 if
- *     unknown.
+ *     the largest of lens; both only shape the launch (speed, and the order of sums),
+ *     0 if unknown: then every sequence is planned for with `rows` rows (where starts
+ *     are given) and its whole capacity. Give them where they are known: attention
+ *     of 64 single tokens with starts took 5 times as long without.
  * Contents are not trusted with memory: a page outside [0, num_pages) holds no
  * position (nothing is written to it, it reads back as zeros, attention does
  * not see it), lens are clamped to [0, capacity] and starts to [0, rows], and a
@@ -559,12 +561,14 @@ int w4_kv_read(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows
  * 0); its contents on entry do not matter, on return they are unspecified. Calls
  * sharing a workspace must not overlap.
  * A row's result depends on nothing but what the row sees: keys and values hidden
- * from it may be of any size, infinite or NaN. Among those it sees, a weight times
- * value scale under 2^-33 of the row's largest is dropped.
+ * from it may be of any size, infinite or NaN. Among those it sees, weights under
+ * 2^-126 of the largest count as 0, and of a weight times value scale what is under
+ * 2^-33 of the largest such product is dropped.
  * Softmax statistics and sums are fp32; the products run on the matrix cores
- * with the codes as exact 16-bit integers, a bf16 query exact and an fp32 one
- * in two pieces of 11 bits. Deterministic for given arguments; max_rows and
- * max_len may change the order of sums.
+ * with the codes as exact 16-bit integers, a bf16 query exact to 2^-35 of its
+ * largest element, an fp32 one in two pieces of 11 bits, and weights times value
+ * scales in 11 bits, or in two such pieces where q or out is fp32. Deterministic
+ * for given arguments; max_rows and max_len may change the order of sums.
  */
 size_t w4_kv_attention_workspace_bytes(const w4_kv_pages* cache, const w4_kv_batch* batch,
                                        int64_t Hq, int64_t window, int64_t sinks);
