@@ -264,7 +264,8 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvPages c, KvAttn a, int s
     constexpr int PF = kv_partial_floats(D), LANES = D / 4, SIDE = 64 / LANES, kAhead = 8;
     const int lane = threadIdx.x & 63;
     const int64_t vectors = (int64_t)c.rows * a.Hq;
-    for (int64_t v = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); v < vectors; v += (int64_t)gridDim.x * 4) {  // whole wavefronts
+    // whole wavefronts
+    for (int64_t v = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); v < vectors; v += (int64_t)gridDim.x * 4) {
         const int row = (int)(v / a.Hq), h = (int)(v - (int64_t)row * a.Hq);
         const float* w = static_cast<const float*>(a.work) + v * splits * PF;
         const int mine = min(lane, splits - 1), side = lane / LANES, e0 = 4 * (lane % LANES);
