@@ -11,6 +11,8 @@ Schemes (see include/w4a16.h):
   "aff4_g64"   affine 4-bit, 64 weights/group, bf16 scale + bf16 bias
                (TurboFieldfare article, section 量化和精度)
   "aff8_g64"   the same affine format with 8-bit codes (the router)
+  "mx4_g32"    microscaled 4-bit floating point: E2M1 codes, 32 weights/group, one
+               exponent byte per group (the mx4_* functions)
 """
 from __future__ import annotations
 
@@ -25,9 +27,10 @@ __all__ = [
     "SCHEME_IDS", "W4Error", "QuantizedMatrix", "lib", "lib_path", "packed_sizes", "quantize_pack",
     "empty_quantized", "gemv", "gemv_into", "gemv_multi", "gemv_multi_into", "gemm", "moe_route", "moe_workspace_bytes", "moe_gemv",
     "KVPages", "KVBatch", "kv_pages", "kv_write", "kv_read", "kv_attention", "kv_attention_workspace",
+    "mx4_quantize", "mx4_read", "mx4_gemm", "mx4_gemm_workspace", "moe_select", "mx4_moe", "mx4_moe_workspace",
 ]
 
-SCHEME_IDS = {"sym4_g128": 0, "aff4_g64": 1, "aff8_g64": 2}
+SCHEME_IDS = {"sym4_g128": 0, "aff4_g64": 1, "aff8_g64": 2, "mx4_g32": 3}
 _ERRORS = {-1: "W4_EINVAL", -2: "W4_ESHAPE", -3: "W4_EALIGN", -4: "W4_EHIP", -5: "W4_EWORKSPACE"}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -62,6 +65,12 @@ class _W4KvBatch(ctypes.Structure):
 class _W4Rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("row_stride", ctypes.c_int64),
                 ("head_stride", ctypes.c_int64)]
+
+
+class _W4Select(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("top_k", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -119,6 +128,18 @@ _SIGS = {
     "w4a16_moe_gemv_logits": ([ctypes.POINTER(_W4Matrix)] * 6 + [_P, _I64, _P, ctypes.c_int, _P, _P,
                                                                  _P, ctypes.c_size_t, _P, _P],
                               ctypes.c_int),
+    "w4_mx4_quantize": ([ctypes.POINTER(_W4Rows), _I64, _I64, _P, _P, _P], ctypes.c_int),
+    "w4_mx4_read": ([ctypes.POINTER(_W4Matrix), ctypes.POINTER(_W4Rows), _P], ctypes.c_int),
+    "w4_mx4_gemm_workspace_bytes": ([ctypes.POINTER(_W4Matrix), _I64, ctypes.c_int], ctypes.c_size_t),
+    "w4_mx4_gemm": ([ctypes.POINTER(_W4Matrix), ctypes.POINTER(_W4Rows), _I64, ctypes.POINTER(_W4Rows), _P,
+                     ctypes.c_size_t, _P], ctypes.c_int),
+    "w4a4_mx4_gemm": ([ctypes.POINTER(_W4Matrix), ctypes.POINTER(_W4Matrix), ctypes.POINTER(_W4Rows), _P,
+                       ctypes.c_size_t, _P], ctypes.c_int),
+    "w4_moe_select": ([ctypes.POINTER(_W4Rows), _I64, _I64, ctypes.POINTER(_W4Select), _P, _P, _P], ctypes.c_int),
+    "w4_mx4_moe_workspace_bytes": ([_I64, ctypes.c_int, _I64, _I64, _I64], ctypes.c_size_t),
+    "w4_mx4_moe": ([ctypes.POINTER(_W4Matrix)] * 3 + [ctypes.POINTER(_W4Rows), _I64, _P, _P, ctypes.c_int,
+                                                      ctypes.c_int, ctypes.POINTER(_W4Rows), _P, ctypes.c_size_t,
+                                                      _P], ctypes.c_int),
 }
 
 
@@ -173,9 +194,9 @@ def packed_sizes(scheme: str, N: int, K: int):
 class QuantizedMatrix:
     """Storage form of one quantized matrix (or a fixed-stride stack of experts).
 
-    codes: uint8 [E][N][K*bits/8]; scale: fp32 [E][N][K/128] (sym) or bf16
-    [E][N][K/64]; bias: bf16 [E][N][K/64] or None. E = num_experts (leading
-    dimension omitted when 1)."""
+    codes: uint8 [E][N][K*bits/8]; scale: fp32 [E][N][K/128] (sym), bf16
+    [E][N][K/64] (affine) or uint8 [E][N][K/32] (mx4); bias: bf16 [E][N][K/64] or None. E =
+    num_experts (leading dimension omitted when 1)."""
     scheme: str
     N: int
     K: int
@@ -206,6 +227,9 @@ def empty_quantized(scheme: str, N: int, K: int, num_experts: int = 1, device="c
     codes = torch.empty(lead + (N, K * bits // 8), dtype=torch.uint8, device=device)
     if scheme == "sym4_g128":
         scale = torch.empty(lead + (N, K // 128), dtype=torch.float32, device=device)
+        bias = None
+    elif scheme == "mx4_g32":
+        scale = torch.empty(lead + (N, K // 32), dtype=torch.uint8, device=device)
         bias = None
     else:
         scale = torch.empty(lead + (N, K // 64), dtype=torch.bfloat16, device=device)
@@ -655,6 +679,186 @@ def kv_attention(q: torch.Tensor, cache: KVPages, batch: KVBatch, scale: Optiona
              cache.D ** -0.5 if scale is None else scale, window, sinks, do, plse, workspace.data_ptr() or None,
              workspace.nbytes)
     return out if lse is None else (out, lse)
+
+
+# ---------------------------------------------------------------- microscaled 4-bit
+def _mx4_rows(t: torch.Tensor, name: str, rows: Optional[int], width: Optional[int], types=_ROW_TYPES) -> _W4Rows:
+    """w4_rows of a device tensor [rows][width], contiguous along its rows."""
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}][{'columns' if width is None else width}],"
+                         f" not {tuple(t.shape)}")
+    code = types.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be {' or '.join(str(d).split('.')[1] for d in types)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous along its rows")
+    return _W4Rows(t.data_ptr(), code, t.stride(0), 0)
+
+
+_BF16_ROWS = {torch.bfloat16: 1}
+
+
+def _mx4_matrix(q: QuantizedMatrix, name: str, index: Optional[int] = None) -> _W4Matrix:
+    """The descriptor of a microscaled matrix, its tensors checked against its sizes."""
+    if q.scheme != "mx4_g32":
+        raise ValueError(f"{name} is {q.scheme}, not mx4_g32")
+    c, s = q.codes, q.scale
+    if c.dtype != torch.uint8 or s.dtype != torch.uint8 or not c.is_cuda or not s.is_cuda \
+            or not c.is_contiguous() or not s.is_contiguous():
+        raise ValueError(f"{name}: codes and scale must be contiguous uint8 device tensors")
+    n = q.num_experts * q.N
+    if 2 * c.numel() != n * q.K or 32 * s.numel() != n * q.K:
+        raise ValueError(f"{name}: codes {tuple(c.shape)} and scale {tuple(s.shape)} for {q.num_experts} x [{q.N}][{q.K}]")
+    d = c.get_device()
+    if s.get_device() != d or (index is not None and d != index):
+        raise ValueError(f"{name} is on more than one device, or on another one")
+    return q.desc()
+
+
+def _on(index: int, f, *args) -> None:
+    """f(*args, stream) on device `index` and its current stream."""
+    if torch.cuda.current_device() == index:
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        _check(rc)
+
+
+def _same_device(index: int, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, the call on cuda:{index}")
+
+
+def mx4_quantize(x: torch.Tensor, out: Optional[QuantizedMatrix] = None) -> QuantizedMatrix:
+    """Rows x [rows][K] (fp32 or bf16, strided) in the microscaled 4-bit format: weights, or activations
+    for mx4_gemm (into `out`, a matrix of that shape, if given)."""
+    d = _mx4_rows(x, "x", None, None)
+    rows, K = x.shape
+    if out is None:
+        out = empty_quantized("mx4_g32", rows, K, device=x.device)
+    elif (out.N, out.K, out.num_experts) != (rows, K, 1):
+        raise ValueError(f"out is {out.num_experts} x [{out.N}][{out.K}], x [{rows}][{K}]")
+    index = x.get_device()
+    _mx4_matrix(out, "out", index)
+    _on(index, lib().w4_mx4_quantize, d, rows, K, _ptr(out.codes), _ptr(out.scale))
+    return out
+
+
+def mx4_read(q: QuantizedMatrix, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values of a microscaled matrix: [N][K] of `dtype` (fp32 or bf16), or into `out` (strided)."""
+    m = _mx4_matrix(q, "q")
+    if out is None:
+        out = torch.empty((q.N, q.K), dtype=dtype, device=q.codes.device)
+    d = _mx4_rows(out, "out", q.N, q.K)
+    index = q.codes.get_device()
+    _same_device(index, out=out)
+    _on(index, lib().w4_mx4_read, m, d)
+    return out
+
+
+def mx4_gemm_workspace(W: QuantizedMatrix, M: int, x4: bool = False) -> torch.Tensor:
+    """A workspace for mx4_gemm of M rows (x4: of quantized rows); empty where it needs none."""
+    n = int(lib().w4_mx4_gemm_workspace_bytes(_mx4_matrix(W, "W"), M, int(x4)))
+    return torch.empty(n, dtype=torch.uint8, device=W.codes.device)
+
+
+def mx4_gemm(W: QuantizedMatrix, X, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y [M][N] = X [M][K] times the microscaled W [N][K] transposed. X: bf16 rows (strided), or a
+    QuantizedMatrix of M rows (mx4_quantize), which multiplies 4 bits by 4 bits. Y: `dtype` (bf16 or
+    fp32), or into `out` (strided). One row or many; workspace: mx4_gemm_workspace(...)'s (allocated for the
+    call by default); calls that may overlap need their own."""
+    index = W.codes.get_device()
+    w = _mx4_matrix(W, "W")
+    x4 = isinstance(X, QuantizedMatrix)
+    M = X.N if x4 else X.shape[0]
+    x = _mx4_matrix(X, "X", index) if x4 else _mx4_rows(X, "X", None, W.K, _BF16_ROWS)
+    if out is None:
+        out = torch.empty((M, W.N), dtype=dtype, device=W.codes.device)
+    y = _mx4_rows(out, "out", M, W.N)
+    if workspace is None:
+        workspace = mx4_gemm_workspace(W, M, x4)
+    elif not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    _same_device(index, X=None if x4 else X, out=out, workspace=workspace)
+    wp, wb = workspace.data_ptr() or None, workspace.nbytes
+    if x4:
+        _on(index, lib().w4a4_mx4_gemm, w, x, y, wp, wb)
+    else:
+        _on(index, lib().w4_mx4_gemm, w, x, M, y, wp, wb)
+    return out
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_ACTS = {"gelu_tanh": 0, "silu": 1}
+
+
+def moe_select(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+               groups: int = 1, top_groups: int = 1, group_best: int = 1, renormalize: bool = False,
+               scale: float = 1.0, ids: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None):
+    """(ids int32, weights fp32), both [M][top_k], of router logits [M][E] (fp32 or bf16, strided): softmax or
+    sigmoid scores, a bias [E] that only the choice sees, experts of the top_groups best of `groups`
+    groups (by the sum of their group_best largest choice values), weights renormalized and scaled
+    (w4_moe_select in include/w4a16.h)."""
+    d = _mx4_rows(logits, "logits", None, None)
+    M, E = logits.shape
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {', '.join(_SCORES)}")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,) or not bias.is_contiguous()):
+        raise ValueError(f"bias must be contiguous float32 [{E}]")
+    if ids is None:
+        ids = torch.empty((M, top_k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((M, top_k), dtype=torch.float32, device=logits.device)
+    for t, name, dt in ((ids, "ids", torch.int32), (weights, "weights", torch.float32)):
+        if t.dtype != dt or t.shape != (M, top_k) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {dt} [{M}][{top_k}]")
+    index = logits.get_device()
+    _same_device(index, bias=bias, ids=ids, weights=weights)
+    how = _W4Select(_SCORES[score], top_k, groups, top_groups, group_best, int(bool(renormalize)), scale, _ptr(bias))
+    _on(index, lib().w4_moe_select, d, M, E, how, ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def mx4_moe_workspace(gate: QuantizedMatrix, up: QuantizedMatrix, down: QuantizedMatrix, M: int,
+                      top_k: int) -> torch.Tensor:
+    """A workspace for mx4_moe with these stacks, M tokens and top_k experts a token."""
+    n = int(lib().w4_mx4_moe_workspace_bytes(M, top_k, gate.num_experts, gate.K, gate.N))
+    return torch.empty(n, dtype=torch.uint8, device=gate.codes.device)
+
+
+def mx4_moe(gate: QuantizedMatrix, up: QuantizedMatrix, down: QuantizedMatrix, x: torch.Tensor,
+            ids: torch.Tensor, weights: torch.Tensor, act: str = "gelu_tanh", out: Optional[torch.Tensor] = None,
+            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y bf16 [M][D]: the gated FFN of each token's experts ids [M][top_k] (int32; outside [0, E): none), weighted
+    by weights [M][top_k] (fp32) and added up, for x bf16 [M][D] (strided) and microscaled stacks
+    gate, up [E][F][D], down [E][D][F]. Any number of tokens. workspace: mx4_moe_workspace(...)'s."""
+    index = gate.codes.get_device()
+    mats = [_mx4_matrix(q, n, index) for q, n in ((gate, "gate"), (up, "up"), (down, "down"))]
+    dx = _mx4_rows(x, "x", None, gate.K, _BF16_ROWS)
+    M = x.shape[0]
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}")
+    if ids.dim() != 2 or ids.shape[0] != M or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError(f"ids must be contiguous int32 [{M}][top_k]")
+    if weights.shape != ids.shape or weights.dtype != torch.float32 or not weights.is_contiguous():
+        raise ValueError("weights must be contiguous float32 of the shape of ids")
+    if out is None:
+        out = torch.empty((M, gate.K), dtype=torch.bfloat16, device=x.device)
+    dy = _mx4_rows(out, "out", M, gate.K, _BF16_ROWS)
+    if workspace is None:
+        workspace = mx4_moe_workspace(gate, up, down, M, ids.shape[1])
+    elif not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    _same_device(index, x=x, ids=ids, weights=weights, out=out, workspace=workspace)
+    _on(index, lib().w4_mx4_moe, *mats, dx, M, ids.data_ptr(), weights.data_ptr(), ids.shape[1], _ACTS[act], dy,
+        workspace.data_ptr() or None, workspace.nbytes)
+    return out
 
 
 MOE_SCRATCH_BYTES = 16 << 20

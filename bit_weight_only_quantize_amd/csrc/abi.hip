@@ -11,6 +11,7 @@
 #include "../../include/w4a16.h"
 #include "kv_attention.hpp"
 #include "launch.hpp"
+#include "mx4.hpp"
 
 namespace {
 
@@ -72,6 +73,15 @@ const char* w4_last_error(void) { return g_err; }
 
 int w4_packed_sizes(int scheme, int64_t N, int64_t K, size_t* codes_bytes, size_t* scale_bytes,
                     size_t* bias_bytes) {
+    if (scheme == W4_MX4_G32) {
+        if (N < 0 || K < 0 || K % w4::kMxGroup)
+            return fail(W4_ESHAPE, "N=%lld K=%lld (K must be a multiple of %d)", (long long)N, (long long)K,
+                        w4::kMxGroup);
+        if (codes_bytes) *codes_bytes = (size_t)N * (size_t)(K / 2);
+        if (scale_bytes) *scale_bytes = (size_t)N * (size_t)(K / w4::kMxGroup);
+        if (bias_bytes) *bias_bytes = 0;
+        return ok();
+    }
     if (!known(scheme)) return fail(W4_EINVAL, "unknown scheme %d", scheme);
     if (N < 0 || K < 0 || K % group_of(scheme))
         return fail(W4_ESHAPE, "N=%lld K=%lld (K must be a multiple of %d)", (long long)N,
@@ -85,6 +95,10 @@ int w4_packed_sizes(int scheme, int64_t N, int64_t K, size_t* codes_bytes, size_
 
 int w4_quantize_pack(int scheme, const float* W, int64_t N, int64_t K, void* codes, void* scale,
                      void* bias, void* stream) {
+    if (scheme == W4_MX4_G32) {
+        const w4_rows x = {(void*)W, W4_F32, K, 0};
+        return w4_mx4_quantize(&x, N, K, codes, scale, stream);
+    }
     if (!known(scheme)) return fail(W4_EINVAL, "unknown scheme %d", scheme);
     if (N < 0 || K <= 0 || K % group_of(scheme))
         return fail(W4_ESHAPE, "N=%lld K=%lld (K must be a positive multiple of %d)",
@@ -969,6 +983,202 @@ int w4_kv_attention(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4
     return hip_status(w4::launch_kv_attention(cache->D, q->dtype == W4_BF16, out->dtype == W4_BF16, v, a,
                                               (hipStream_t)stream),
                       "kv_attention launch");
+}
+
+// ---------------------------------------------------------------- microscaled 4-bit
+// One matrix, or a stack of any number of them (experts == 0)
+static int mx4_check(const w4_matrix* W, const char* name, int experts) {
+    if (!W) return fail(W4_EINVAL, "%s: null descriptor", name);
+    if (W->scheme != W4_MX4_G32) return fail(W4_EINVAL, "%s: scheme %d, not W4_MX4_G32", name, (int)W->scheme);
+    if (W->num_experts < 1 || (experts && W->num_experts != experts))
+        return fail(W4_ESHAPE, "%s: num_experts %d", name, (int)W->num_experts);
+    if (W->N < 0 || W->K <= 0 || W->N > kInt31 || W->K > kInt31 || W->K % w4::kMxGroup)
+        return fail(W4_ESHAPE, "%s: N=%lld K=%lld (K must be a multiple of %d, both under 2^31)", name,
+                    (long long)W->N, (long long)W->K, w4::kMxGroup);
+    if (W->N == 0) return W4_OK;
+    if (!W->codes || !W->scale) return fail(W4_EINVAL, "%s: null codes or scale", name);
+    if (!aligned16(W->codes)) return fail(W4_EALIGN, "%s: codes must be 16-byte aligned", name);
+    return W4_OK;
+}
+
+static w4::Mx4Mat mx4_mat(const w4_matrix* W) {
+    return {(const uint8_t*)W->codes, (const uint8_t*)W->scale, W->N, W->K};
+}
+
+// Rows of `width` elements; `vectors`: the kernel moves 16 bytes at a time along them
+static int mx4_check_rows(const w4_rows* t, const char* name, int64_t rows, int64_t width, bool vectors,
+                          bool bf16_only) {
+    if (!t) return fail(W4_EINVAL, "%s: null descriptor", name);
+    if (!t->data) return fail(W4_EINVAL, "%s: null data", name);
+    if (t->dtype != W4_BF16 && (bf16_only || t->dtype != W4_F32))
+        return fail(W4_EINVAL, "%s: type %d", name, (int)t->dtype);
+    if (!aligned16(t->data)) return fail(W4_EALIGN, "%s must be 16-byte aligned", name);
+    if (rows <= 1) return W4_OK;
+    if (t->row_stride < width || t->row_stride > (1LL << 40))
+        return fail(W4_ESHAPE, "%s: row stride %lld for %lld columns", name, (long long)t->row_stride,
+                    (long long)width);
+    if (vectors && t->row_stride % (t->dtype == W4_BF16 ? 8 : 4))
+        return fail(W4_EALIGN, "%s: row stride %lld must be a multiple of 16 bytes", name,
+                    (long long)t->row_stride);
+    return W4_OK;
+}
+
+int w4_mx4_quantize(const w4_rows* x, int64_t rows, int64_t K, void* codes, void* scale, void* stream) {
+    if (rows < 0 || rows > kInt31 || K <= 0 || K > kInt31 || K % w4::kMxGroup)
+        return fail(W4_ESHAPE, "rows=%lld K=%lld (K must be a positive multiple of %d, both under 2^31)",
+                    (long long)rows, (long long)K, w4::kMxGroup);
+    if (rows == 0) return ok();
+    if (!codes || !scale) return fail(W4_EINVAL, "null codes or scale");
+    const int rc = mx4_check_rows(x, "x", rows, K, true, false);
+    if (rc) return rc;
+    if (!aligned16(codes)) return fail(W4_EALIGN, "codes must be 16-byte aligned");
+    return hip_status(w4::launch_mx4_quantize(x->data, x->dtype == W4_BF16, x->row_stride, rows, K,
+                                              (uint8_t*)codes, (uint8_t*)scale, (hipStream_t)stream),
+                      "mx4_quantize launch");
+}
+
+int w4_mx4_read(const w4_matrix* q, const w4_rows* out, void* stream) {
+    int rc = mx4_check(q, "q", 1);
+    if (rc) return rc;
+    if (q->N == 0) return ok();
+    if ((rc = mx4_check_rows(out, "out", q->N, q->K, true, false))) return rc;
+    return hip_status(w4::launch_mx4_read(mx4_mat(q), out->data, out->dtype == W4_BF16, out->row_stride,
+                                          (hipStream_t)stream),
+                      "mx4_read launch");
+}
+
+size_t w4_mx4_gemm_workspace_bytes(const w4_matrix* W, int64_t M, int x4) {
+    if (!W || W->scheme != W4_MX4_G32 || W->num_experts != 1 || W->N <= 0 || W->N > kInt31 || W->K <= 0 ||
+        W->K > kInt31 || W->K % w4::kMxGroup || M <= 0 || M > kInt31)
+        return 0;
+    return w4::mx4_gemm_workspace(M, W->N, W->K, x4 != 0);
+}
+
+static int mx4_gemm_call(const w4_matrix* W, const w4::Mx4X& X, int64_t M, const w4_rows* Y, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    const int rc = mx4_check_rows(Y, "Y", M, W->N, false, false);
+    if (rc) return rc;
+    const size_t need = w4::mx4_gemm_workspace(M, W->N, W->K, X.x == nullptr);
+    if (workspace_bytes && !workspace) return fail(W4_EWORKSPACE, "%zu bytes of no workspace", workspace_bytes);
+    if (workspace && workspace_bytes && workspace_bytes < need)
+        return fail(W4_EWORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    if (need && workspace && !aligned16(workspace)) return fail(W4_EALIGN, "workspace must be 16-byte aligned");
+    return hip_status(w4::launch_mx4_gemm(mx4_mat(W), X, M, Y->data, Y->dtype == W4_BF16, Y->row_stride,
+                                          need && workspace_bytes ? workspace : nullptr, (hipStream_t)stream),
+                      "mx4_gemm launch");
+}
+
+int w4_mx4_gemm(const w4_matrix* W, const w4_rows* X, int64_t M, const w4_rows* Y, void* workspace,
+                size_t workspace_bytes, void* stream) {
+    int rc = mx4_check(W, "W", 1);
+    if (rc) return rc;
+    if (M < 0 || M > kInt31) return fail(W4_ESHAPE, "M=%lld out of range", (long long)M);
+    if (M == 0 || W->N == 0) return ok();
+    if ((rc = mx4_check_rows(X, "X", M, W->K, true, true))) return rc;
+    return mx4_gemm_call(W, {(const uint16_t*)X->data, M > 1 ? X->row_stride : W->K, nullptr, nullptr}, M, Y,
+                         workspace, workspace_bytes, stream);
+}
+
+int w4a4_mx4_gemm(const w4_matrix* W, const w4_matrix* X, const w4_rows* Y, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+    int rc = mx4_check(W, "W", 1);
+    if (rc || (rc = mx4_check(X, "X", 1))) return rc;
+    if (X->K != W->K) return fail(W4_ESHAPE, "X has K=%lld, W K=%lld", (long long)X->K, (long long)W->K);
+    if (X->N == 0 || W->N == 0) return ok();
+    return mx4_gemm_call(W, {nullptr, 0, (const uint8_t*)X->codes, (const uint8_t*)X->scale}, X->N, Y, workspace,
+                         workspace_bytes, stream);
+}
+
+int w4_moe_select(const w4_rows* logits, int64_t M, int64_t E, const w4_select* how, int32_t* ids,
+                  float* weights, void* stream) {
+    if (!how) return fail(W4_EINVAL, "null selection");
+    if (how->score != W4_SCORE_SOFTMAX && how->score != W4_SCORE_SIGMOID)
+        return fail(W4_EINVAL, "unknown score %d", (int)how->score);
+    if (M < 0 || M > kInt31 || E < 1 || E > 1024)
+        return fail(W4_ESHAPE, "M=%lld E=%lld out of range", (long long)M, (long long)E);
+    const int G = how->groups;
+    if (G < 1 || G > 64 || E % G || how->top_groups < 1 || how->top_groups > G)
+        return fail(W4_ESHAPE, "groups=%d top_groups=%d for E=%lld", G, (int)how->top_groups, (long long)E);
+    if (how->group_best < 1 || how->group_best > 2 || how->group_best > E / G)
+        return fail(W4_ESHAPE, "group_best=%d for groups of %lld", (int)how->group_best, (long long)(E / G));
+    if (how->top_k < 1 || how->top_k > 32 || how->top_k > how->top_groups * (E / G))
+        return fail(W4_ESHAPE, "top_k=%d of %lld experts", (int)how->top_k, (long long)(how->top_groups * (E / G)));
+    if (!isfinite(how->scale)) return fail(W4_EINVAL, "scale is not finite");
+    if (M == 0) return ok();
+    const int rc = mx4_check_rows(logits, "logits", M, E, false, false);
+    if (rc) return rc;
+    if (!ids || !weights) return fail(W4_EINVAL, "null ids or weights");
+    if (!aligned16(ids) || !aligned16(weights) || (how->bias && !aligned16(how->bias)))
+        return fail(W4_EALIGN, "ids, weights and bias must be 16-byte aligned");
+    w4::SelectArgs a;
+    a.logits = logits->data;
+    a.row_stride = logits->row_stride;
+    a.bias = how->bias;
+    a.ids = ids;
+    a.weights = weights;
+    a.M = M;
+    a.E = (int)E;
+    a.k = how->top_k;
+    a.sigmoid = how->score == W4_SCORE_SIGMOID;
+    a.groups = how->top_groups == G ? 1 : G;  // where all groups are kept, they choose nothing
+    a.top_groups = how->top_groups;
+    a.best = how->group_best;
+    a.renormalize = how->renormalize != 0;
+    a.scale = how->scale;
+    return hip_status(w4::launch_moe_select(a, logits->dtype == W4_BF16, (hipStream_t)stream), "moe_select launch");
+}
+
+static const int64_t kMoePairs = 1 << 24;
+
+size_t w4_mx4_moe_workspace_bytes(int64_t M, int top_k, int64_t E, int64_t D, int64_t F) {
+    if (M <= 0 || top_k < 1 || top_k > 32 || M > kMoePairs / top_k || E < 1 || E > 1024 || D < 1 || F < 1 ||
+        D > kInt31 || F > kInt31)
+        return 0;
+    return w4::mx4_moe_workspace(M, top_k, E, D, F);
+}
+
+int w4_mx4_moe(const w4_matrix* gate, const w4_matrix* up, const w4_matrix* down, const w4_rows* x,
+               int64_t M, const int32_t* ids, const float* weights, int top_k, int act,
+               const w4_rows* y, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = mx4_check(gate, "gate", 0);
+    if (rc || (rc = mx4_check(up, "up", 0)) || (rc = mx4_check(down, "down", 0))) return rc;
+    const int64_t E = gate->num_experts, F = gate->N, D = gate->K;
+    if (up->num_experts != E || down->num_experts != E)
+        return fail(W4_ESHAPE, "gate, up and down must have the same number of experts");
+    if (up->N != F || up->K != D || down->N != D || down->K != F)
+        return fail(W4_ESHAPE, "expected gate/up [E][F][D] and down [E][D][F]");
+    if (E > 1024) return fail(W4_ESHAPE, "E=%lld exceeds 1024", (long long)E);
+    if (act != W4_ACT_GELU_TANH && act != W4_ACT_SILU) return fail(W4_EINVAL, "unknown activation %d", act);
+    if (top_k < 1 || top_k > 32) return fail(W4_ESHAPE, "top_k=%d out of range [1, 32]", top_k);
+    if (M < 0 || M > kMoePairs / top_k)
+        return fail(W4_ESHAPE, "M=%lld: M * top_k at most 2^24", (long long)M);
+    if (M == 0) return ok();
+    if ((rc = mx4_check_rows(x, "x", M, D, true, true)) || (rc = mx4_check_rows(y, "y", M, D, false, true)))
+        return rc;
+    if (!ids || !weights) return fail(W4_EINVAL, "null ids or weights");
+    if (!aligned16(ids) || !aligned16(weights)) return fail(W4_EALIGN, "ids and weights must be 16-byte aligned");
+    const size_t need = w4::mx4_moe_workspace(M, top_k, E, D, F);
+    if (!workspace || workspace_bytes < need)
+        return fail(W4_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                    workspace ? workspace_bytes : (size_t)0);
+    if (!aligned16(workspace)) return fail(W4_EALIGN, "workspace must be 16-byte aligned");
+    w4::Mx4Moe a;
+    a.gate = mx4_mat(gate);
+    a.up = mx4_mat(up);
+    a.down = mx4_mat(down);
+    a.E = (int)E;
+    a.k = top_k;
+    a.act = act;
+    a.M = M;
+    a.D = D;
+    a.F = F;
+    a.x = (const uint16_t*)x->data;
+    a.x_stride = M > 1 ? x->row_stride : D;
+    a.ids = ids;
+    a.weights = weights;
+    a.y = (uint16_t*)y->data;
+    a.y_stride = y->row_stride;
+    return hip_status(w4::launch_mx4_moe(a, workspace, (hipStream_t)stream), "mx4_moe launch");
 }
 
 }  // extern "C"

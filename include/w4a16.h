@@ -63,6 +63,7 @@ extern "C" {
 #define W4_SYM4_G128 0 /* symmetric 4-bit, group 128, fp32 scale = absmax/7 [airllm] §4.2 */
 #define W4_AFF4_G64  1 /* affine 4-bit, group 64, bf16 scale + bf16 bias [TurboFieldfare] 量化和精度 */
 #define W4_AFF8_G64  2 /* affine 8-bit, group 64, bf16 scale + bf16 bias (router) [TurboFieldfare] 量化和精度 */
+#define W4_MX4_G32   3 /* microscaled 4-bit floating point, group 32, one exponent byte (the w4_mx4 and w4a4 calls) */
 
 /*
  * A quantized matrix, or a stack of `num_experts` matrices of identical shape
@@ -575,6 +576,105 @@ size_t w4_kv_attention_workspace_bytes(const w4_kv_pages* cache, const w4_kv_bat
 int w4_kv_attention(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4_rows* q,
                     int64_t Hq, float scale, int64_t window, int64_t sinks, const w4_rows* out,
                     float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Microscaled 4-bit floating point (W4_MX4_G32): the E2M1 / E8M0 block format of
+ * the OCP Microscaling Formats specification 1.0, groups of 32 along K.
+ * codes uint8 [N][K / 2], element 2j in the low nibble of byte j: sign, two exponent
+ * bits, one mantissa bit, i.e. 0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives (8 to
+ * 15). scale uint8 [N][K / 32], at any address: byte b stands for 2^(b - 127), 255 for
+ * NaN. No bias array. A value is code times scale. K is a multiple of 32.
+ * w4_packed_sizes and w4_quantize_pack (fp32 [N][K]) take the scheme too; the other
+ * calls of the sections above do not (W4_EINVAL).
+ *
+ * Quantization of a group with largest magnitude a: scale 2^(floor(log2 a) - 2), not
+ * under 2^-127; codes nearest to value / scale, ties to the even code, magnitudes
+ * over 6 to 6. A group with an infinity or a NaN gets scale 255 and codes 0, so that
+ * it reads back as NaN. Bit-exact: only exact steps before the rounding.
+ *
+ * Rows are described by w4_rows with one head: element (r, i) at data + r *
+ * row_stride + i (head_stride is not looked at). Rows that these calls read are
+ * 16-byte aligned, their stride a multiple of 16 bytes (any for a single row); of rows
+ * that are written, only data has to be 16-byte aligned where nothing else is said.
+ */
+
+/* x [rows][K], fp32 or bf16, to codes and scale of one matrix of `rows` rows. 0 <= rows < 2^31. */
+int w4_mx4_quantize(const w4_rows* x, int64_t rows, int64_t K, void* codes, void* scale, void* stream);
+
+/* The values of q (one matrix) to out [N][K], fp32 or bf16 (exact in both, but for
+ * bf16 numbers under 2^-133), a multiple of 16 bytes from row to row. */
+int w4_mx4_read(const w4_matrix* q, const w4_rows* out, void* stream);
+
+/*
+ * Y [M][N] = X [M][K] W^T with the weights unpacked in the kernels: X bf16 rows
+ * (w4_mx4_gemm), or X quantized to the same format, one matrix of M rows
+ * (w4a4_mx4_gemm: both sides in 4 bits go to the matrix cores as they are stored).
+ * Y: fp32 or bf16 (nearest even), Y's row_stride >= N. Products are exact and sums
+ * fp32; a row of X with an infinity or NaN gives what the sum gives, a NaN scale
+ * NaN. W: one matrix. M, N < 2^31 and any size down to 0; K < 2^31. Any number of
+ * rows takes the same call: few rows stream the weights, many fill matrix tiles.
+ * workspace: w4_mx4_gemm_workspace_bytes(...) bytes (x4: whether X is quantized), 0 for
+ * most sizes; contents on entry do not matter. Without it (NULL and 0 bytes) the
+ * product takes fewer workgroups and longer. Y must not overlap the inputs. Deterministic;
+ * the order of sums depends on the sizes, and on whether there is a workspace.
+ */
+size_t w4_mx4_gemm_workspace_bytes(const w4_matrix* W, int64_t M, int x4);
+int w4_mx4_gemm(const w4_matrix* W, const w4_rows* X, int64_t M, const w4_rows* Y, void* workspace,
+                size_t workspace_bytes, void* stream);
+int w4a4_mx4_gemm(const w4_matrix* W, const w4_matrix* X, const w4_rows* Y, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/*
+ * Selection of experts from router logits [M][E] (fp32 or bf16 rows; any row stride >=
+ * E), more generally than w4_moe_route. With scores s = softmax(l) or sigmoid(l) of a
+ * token's E logits and choice values c = s + bias:
+ *   groups > 1: group g holds the experts g E / groups ... (g + 1) E / groups - 1; its
+ *     value is the sum of its group_best (1 or 2) largest c; only experts of the
+ *     top_groups groups of largest value can be chosen;
+ *   the top_k experts of largest c are chosen, largest first; without a bias those of
+ *     the largest logits, which is the same order;
+ *   their weights are s, divided by their sum if renormalize, times scale.
+ * Ties go to the lower index. Choices are made on c as 64-bit arithmetic gives it.
+ * An expert whose logit is -infinity is masked: its weight is 0, and it is chosen (and
+ * counts for its group) only after all others; a token whose every logit is masked
+ * gets weights 0. A NaN logit counts as masked and makes the token's weights NaN.
+ * bias fp32 [E] or NULL; 1 <= top_k <= min(32, top_groups * E / groups); E <= 1024;
+ * groups divides E, 1 <= top_groups <= groups <= 64, group_best <= E / groups.
+ * ids int32 [M][top_k], weights fp32 [M][top_k]. 0 <= M < 2^31. Feeds w4a16_moe_gemv and
+ * w4_mx4_moe.
+ */
+#define W4_SCORE_SOFTMAX 0
+#define W4_SCORE_SIGMOID 1
+typedef struct w4_select {
+    int32_t score; /* W4_SCORE_SOFTMAX or W4_SCORE_SIGMOID */
+    int32_t top_k, groups, top_groups, group_best, renormalize;
+    float scale;
+    const float* bias;
+} w4_select;
+int w4_moe_select(const w4_rows* logits, int64_t M, int64_t E, const w4_select* how, int32_t* ids,
+                  float* weights, void* stream);
+
+/*
+ * Mixture-of-experts FFN with microscaled 4-bit weights, for one token up to long
+ * prompts:
+ *   y[m] = sum_j weights[m][j] * W_down[e] h,
+ *   h = bf16(act(W_gate[e] x[m]) * (W_up[e] x[m])),   e = ids[m][j],
+ * with act gelu_tanh (W4_ACT_GELU_TANH, as everywhere above) or silu. gate, up: stacks
+ * [E][F][D]; down [E][D][F]; D and F multiples of 32. x bf16 [M][D]; y bf16 [M][D] with a
+ * row stride >= D, not overlapping x. ids, weights [M][top_k] as w4_moe_select or w4_moe_route give them;
+ * a slot whose id lies outside [0, E) contributes nothing, and a token without any gets
+ * y = 0. An expert's weights are read once for all its tokens (once for 256 of them
+ * or so). Sums are fp32, h and each expert's part of y are
+ * rounded to bf16. 0 <= M, M * top_k <= 2^24, top_k <= 32,
+ * E <= 1024. workspace: w4_mx4_moe_workspace_bytes(...) bytes; its contents on entry do not
+ * matter. Calls sharing a workspace must not overlap. Deterministic.
+ */
+#define W4_ACT_GELU_TANH 0
+#define W4_ACT_SILU 1
+size_t w4_mx4_moe_workspace_bytes(int64_t M, int top_k, int64_t E, int64_t D, int64_t F);
+int w4_mx4_moe(const w4_matrix* gate, const w4_matrix* up, const w4_matrix* down, const w4_rows* x,
+               int64_t M, const int32_t* ids, const float* weights, int top_k, int act,
+               const w4_rows* y, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Message for the last non-zero return on the calling thread ("" if none). */
 const char* w4_last_error(void);
