@@ -31,9 +31,14 @@ namespace w4 {
 typedef __attribute__((address_space(3))) void lds_void;
 typedef const __attribute__((address_space(1))) void gbl_void;
 
-// Waits for this wavefront's loads and LDS reads, then the barrier: after it every wavefront's
-// direct loads are in LDS, and the stage that was read before it may be overwritten. The empty
-// asm keeps memory operations on their side of it.
+template <int V>
+struct Const {
+    static constexpr int v = V;
+};
+
+// Waits until at most this wavefront's last N loads are in flight, then the barrier: after it the
+// direct loads before those are in LDS, every wavefront's. The empty asm keeps memory operations
+// on their side of it.
 template <int N>
 __device__ __forceinline__ void loads_done_barrier() {
     static_assert(N >= 0 && N < 64, "vmcnt");

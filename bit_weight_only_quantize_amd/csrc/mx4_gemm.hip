@@ -1,5 +1,6 @@
 // Products with microscaled 4-bit weights: Y = X W^T.
 #include "mx4_block.hpp"
+#include "mx4_block_x4.hpp"
 #include "mx4_tile.hpp"
 
 namespace w4 {
@@ -38,7 +39,8 @@ struct BlockArgs {
 };
 
 // The 16 sums of a 32 x 32 tile that a lane holds: D[i][j] is in lane j + 32 ((i / 4) % 2), register
-// 4 (i / 8) + i % 4
+// 4 (i / 8) + i % 4. Single bf16 values, 32 lanes a row (pairs of columns by exchange with the
+// neighbouring lane, two rows at a time, took 180 us instead of 167 for 2048 x 11008).
 __device__ __forceinline__ void store_tile(const BlockArgs& a, const f32x16_t& v, int64_t m, int64_t n) {
     if (n >= a.W.N) return;
 #pragma unroll
@@ -52,7 +54,7 @@ __device__ __forceinline__ void store_tile(const BlockArgs& a, const f32x16_t& v
 
 // Consecutive tiles go to one XCD (workgroups are dealt to the eight in turn) and run along W
 // first: they share their rows of X.
-template <int BM, int BN, int WM, int WN>
+template <bool X4, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_block_kernel(BlockArgs a) {
     extern __shared__ __align__(16) uint8_t lds[];
     constexpr int NI = BM / WM / 32, NJ = BN / WN / 32, NW = WM * WN;
@@ -61,19 +63,27 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_block_kernel(BlockArgs a)
     if ((int)(blockIdx.x / 8) >= per || unit >= units) return;
     const int tile = unit / a.parts, z = unit % a.parts;
     const int64_t m0 = (int64_t)(tile / a.tiles_n) * BM, n0 = (int64_t)(tile % a.tiles_n) * BN;
-    const int K = (int)a.W.K, steps = (K + kBlockK - 1) / kBlockK;
+    const int K = (int)a.W.K, steps = (K + (X4 ? kBlockK4 : kBlockK) - 1) / (X4 ? kBlockK4 : kBlockK);
+    const int t0 = (int)((int64_t)steps * z / a.parts), t1 = (int)((int64_t)steps * (z + 1) / a.parts);
     f32x16_t acc[NI][NJ];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16_t{};
-    mx4_block_product<BM, BN, WM, WN>(
-        lds, [&](int r) { return a.X.x + min(m0 + r, a.M - 1) * a.X.row_stride; },
-        [&](int c) {
-            const int64_t n = min(n0 + c, a.W.N - 1);
-            return Mx4Mat{a.W.codes + n * (K / 2), a.W.scale + n * (K / 32), 0, 0};
-        },
-        K, (int)((int64_t)steps * z / a.parts), (int)((int64_t)steps * (z + 1) / a.parts), acc);
+    const auto wcol = [&](int c) {
+        const int64_t n = min(n0 + c, a.W.N - 1);
+        return Mx4Mat{a.W.codes + n * (K / 2), a.W.scale + n * (K / 32), 0, 0};
+    };
+    if constexpr (X4) {
+        const auto xrow = [&](int r) {
+            const int64_t m = min(m0 + r, a.M - 1);
+            return Mx4Mat{a.X.codes + m * (K / 2), a.X.scale + m * (K / 32), 0, 0};
+        };
+        mx4_block_product_x4<BM, BN, WM, WN>(lds, xrow, wcol, K, t0, t1, acc);
+    } else {
+        const auto xrow = [&](int r) { return a.X.x + min(m0 + r, a.M - 1) * a.X.row_stride; };
+        mx4_block_product<BM, BN, WM, WN>(lds, xrow, wcol, K, t0, t1, acc);
+    }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (a.parts > 1) {
         f32x4_t* p = reinterpret_cast<f32x4_t*>(a.part) + ((int64_t)unit * NW + wave) * (NI * NJ * 256) + lane;
@@ -116,14 +126,14 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_block_sum_kernel(BlockArgs a
                n0 + (wave % WN) * (BN / WN) + 32 * (b % NJ) + (lane & 31));
 }
 
-template <int BM, int BN, int WM, int WN>
+template <bool X4, int BM, int BN, int WM, int WN>
 static hipError_t launch_block(BlockArgs a, hipStream_t st) {
     const int64_t tm = (a.M + BM - 1) / BM, tn = (a.W.N + BN - 1) / BN;
     if (tm * tn * a.parts > 0x7fffffff - 8) return hipErrorInvalidValue;
     a.tiles_n = (int)tn;
     a.tiles = (int)(tm * tn);
-    const int lds = kStages * mx4_stage_bytes<BM, BN>();
-    auto kern = mx4_block_kernel<BM, BN, WM, WN>;
+    const int lds = kStages * (X4 ? mx4_stage_bytes_x4<BM, BN>() : mx4_stage_bytes<BM, BN>());
+    auto kern = mx4_block_kernel<X4, BM, BN, WM, WN>;
     (void)hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     hipLaunchKernelGGL(kern, dim3((unsigned)((a.tiles * a.parts + 7) / 8 * 8)), dim3(64 * WM * WN), lds, st, a);
     if (a.parts > 1)
@@ -145,18 +155,25 @@ static const BlockShape kShapes[] = {
     {256, 256, 256, 1.60, 6}, {256, 192, 256, 1.33, 6}, {256, 128, 256, 1.02, 5}, {128, 256, 256, 0.98, 5},
     {128, 128, 512, 1.00, 5}, {64, 128, 768, 0.97, 5},
 };
+// 4 bits on both sides: steps of 128 k (4096 x 12288 rows, K = 16384: 560 us with 256 x 192, then 651,
+// 731, 716 and 1093). 256 x 256 needs more registers than there are and takes 632.
+static const BlockShape kShapesX4[] = {
+    {0, 0, 0, 0, 0}, {256, 192, 256, 1.09, 6}, {256, 128, 256, 0.85, 5}, {128, 256, 256, 0.95, 4},
+    {128, 128, 512, 0.93, 3}, {64, 128, 768, 1.07, 2},
+};
 struct BlockPlan {
     int shape, parts;
 };
 static size_t part_bytes(const BlockShape& s, int64_t M, int64_t N) {
     return (size_t)((M + s.bm - 1) / s.bm * s.bm) * ((N + s.bn - 1) / s.bn * s.bn) * 4;
 }
-static BlockPlan block_plan(int64_t M, int64_t N, int64_t K, bool can_split) {
+static BlockPlan block_plan(int64_t M, int64_t N, int64_t K, bool x4, bool can_split) {
+    const BlockShape* shapes = x4 ? kShapesX4 : kShapes;
     BlockPlan best = {0, 1};
     double least = 1e30;
-    const int64_t steps = (K + kBlockK - 1) / kBlockK;
-    for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
-        const BlockShape& s = kShapes[i];
+    const int64_t steps = x4 ? (K + kBlockK4 - 1) / kBlockK4 : (K + kBlockK - 1) / kBlockK;
+    for (int i = x4 ? 1 : 0; i < 6; ++i) {
+        const BlockShape& s = shapes[i];
         const int64_t tiles = ((M + s.bm - 1) / s.bm) * ((N + s.bn - 1) / s.bn);
         for (int p = 1; p <= 16 && 4 * p <= steps + 3; ++p) {
             if (p > 1 && (!can_split || tiles * p > s.slots)) break;
@@ -177,24 +194,30 @@ static BlockPlan block_plan(int64_t M, int64_t N, int64_t K, bool can_split) {
 static constexpr int64_t kFewRows = 16;
 
 size_t mx4_gemm_workspace(int64_t M, int64_t N, int64_t K, bool x4) {
-    if (x4 || M <= kFewRows) return 0;
-    const BlockPlan p = block_plan(M, N, K, true);
+    if (M <= kFewRows) return 0;
+    const BlockPlan p = block_plan(M, N, K, x4, true);
     return p.parts > 1 ? p.parts * part_bytes(kShapes[p.shape], M, N) : 0;
+}
+
+template <bool X4>
+static hipError_t launch_blocks(int shape, const BlockArgs& a, hipStream_t st) {
+    if constexpr (!X4)
+        if (shape == 0) return launch_block<X4, 256, 256, 2, 4>(a, st);
+    switch (shape) {
+        case 1: return launch_block<X4, 256, 192, 4, 2>(a, st);
+        case 2: return launch_block<X4, 256, 128, 4, 2>(a, st);
+        case 3: return launch_block<X4, 128, 256, 2, 4>(a, st);
+        case 4: return launch_block<X4, 128, 128, 2, 2>(a, st);
+        default: return launch_block<X4, 64, 128, 1, 4>(a, st);
+    }
 }
 
 hipError_t launch_mx4_gemm(const Mx4Mat& W, const Mx4X& X, int64_t M, void* Y, bool y_bf16,
                            int64_t y_stride, void* work, hipStream_t st) {
-    if (X.x && M > kFewRows) {
-        const BlockPlan p = block_plan(M, W.N, W.K, work != nullptr);
+    if (M > kFewRows) {
+        const BlockPlan p = block_plan(M, W.N, W.K, !X.x, work != nullptr);
         const BlockArgs a = {W, X, M, Y, y_stride, y_bf16, 0, 0, p.parts, (float*)work};
-        switch (p.shape) {
-            case 0: return launch_block<256, 256, 2, 4>(a, st);
-            case 1: return launch_block<256, 192, 4, 2>(a, st);
-            case 2: return launch_block<256, 128, 2, 4>(a, st);
-            case 3: return launch_block<128, 256, 2, 4>(a, st);
-            case 4: return launch_block<128, 128, 2, 2>(a, st);
-            default: return launch_block<64, 128, 1, 4>(a, st);
-        }
+        return X.x ? launch_blocks<false>(p.shape, a, st) : launch_blocks<true>(p.shape, a, st);
     }
     const int64_t tm = (M + 15) / 16, tn = (W.N + 15) / 16;
     auto kern = X.x ? mx4_gemm_kernel<false> : mx4_gemm_kernel<true>;
