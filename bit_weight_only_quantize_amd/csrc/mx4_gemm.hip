@@ -1,30 +1,184 @@
 // Products with microscaled 4-bit weights: Y = X W^T.
 #include "mx4_block.hpp"
-#include "mx4_block_x4.hpp"
-#include "mx4_tile.hpp"
+#include "mx4_few.hpp"
+#include "mx4_gemv.hpp"
 
 namespace w4 {
 
-// One wavefront a tile of 16 rows of X and 16 rows of W.
-template <bool X4>
-__global__ __launch_bounds__(64) void mx4_gemm_kernel(Mx4Mat W, Mx4X X, int64_t M, void* __restrict__ Y,
-                                                      bool y_bf16, int64_t y_stride, int tiles_n) {
-    const int lane = threadIdx.x, g = lane >> 4, c = lane & 15;
-    const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * 16, n0 = (int64_t)(blockIdx.x % tiles_n) * 16;
-    const int64_t m = min(m0 + c, M - 1), n = min(n0 + c, W.N - 1);
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    mx4_tile_product<X4>(X4 ? nullptr : X.x + m * X.row_stride, X.codes + m * (W.K / 2),
-                         X.scale + m * (W.K / 32), W.codes + n * (W.K / 2), W.scale + n * (W.K / 32), (int)W.K,
-                         acc);
-    if (n0 + c >= W.N) return;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int64_t row = m0 + 4 * g + r;
-        if (row >= M) break;
-        const int64_t at = row * y_stride + n0 + c;
-        if (y_bf16) static_cast<uint16_t*>(Y)[at] = to_bf16(acc[r]);
-        else static_cast<float*>(Y)[at] = acc[r];
+// ---- one row of bf16 (mx4_gemv.hpp): a row of W a wavefront, two loads in flight, 16 wavefronts. 4096 -> 11008
+// takes 7.5 us, 11008 -> 4096 7.6; two or four rows or four loads a wavefront, or four or eight wavefronts, 7.4 to 9.3.
+constexpr int kGemvWaves = 16;
+__global__ __launch_bounds__(64 * kGemvWaves) void mx4_gemv_kernel(Mx4Mat W, const uint16_t* x, void* __restrict__ Y, int y_bf16) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int K = (int)W.K, V = gemv_vectors(K);
+    const int64_t n = (int64_t)blockIdx.x * kGemvWaves + wave, at = min(n, W.N - 1);
+    GemvStream<1, 2> f;
+    f.groups = K / kMxGroup;
+    f.wc[0] = W.codes + at * (K / 2);
+    f.ws[0] = W.scale + at * (K / 32);
+    float acc[1] = {0.f};
+    f.load(0);
+    gemv_stage(lds, x, K);
+    __syncthreads();
+    f.finish(lds, V, acc);
+    if (lane == 0 && n < W.N) {
+        if (y_bf16) static_cast<uint16_t*>(Y)[n] = to_bf16(acc[0]);
+        else static_cast<float*>(Y)[n] = acc[0];
     }
+}
+
+static constexpr int64_t kGemvMaxK = 65536;  // x in LDS: 128 KiB
+
+static hipError_t launch_gemv1(const Mx4Mat& W, const uint16_t* x, void* Y, bool y_bf16, hipStream_t st) {
+    const int lds = gemv_lds_bytes((int)W.K);
+    (void)hipFuncSetAttribute((const void*)mx4_gemv_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    hipLaunchKernelGGL(mx4_gemv_kernel, dim3((unsigned)((W.N + kGemvWaves - 1) / kGemvWaves)), dim3(64 * kGemvWaves), lds, st,
+                       W, x, Y, y_bf16);
+    return hipGetLastError();
+}
+
+// ---- up to 16 rows of bf16 (mx4_few.hpp): one workgroup of 16 wavefronts a CU owns consecutive
+// tiles of 16 rows of W, `side` of them at a time with 16 / side wavefronts on each one's steps
+// (their sums meet in LDS, in a fixed order), over X staged `chunk` steps at a time. One load of
+// codes in flight a wavefront: 18.5 us for 13 rows, 5120 -> 13824, against 20.7 with two and 21.5 with four; eight
+// wavefronts 20.8. Direct lane loads of X took 20 to 40.
+constexpr int kFewWaves = 16;
+
+
+
+__global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4Mat W, Mx4X X, int M, void* __restrict__ Y,
+                                                                 int y_bf16, int64_t y_stride, int tiles, int side,
+                                                                 int chunk) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    __shared__ f32x4_t sums[kFewWaves][64];
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int K = (int)W.K, steps = (K + 127) / 128, by = kFewWaves / side;
+    const int mine = wave / by, ks = wave % by;
+    const int first = (int)((int64_t)tiles * blockIdx.x / gridDim.x);
+    const int last = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
+    const uint8_t* x = lds + min(c, M - 1) * few_row_bytes(chunk) + 64 * g;
+    FewStream<1, 1> f;
+    f.groups = K / kMxGroup;
+    bool staged = false;
+    for (int t0 = first; t0 < last; t0 += side) {
+        const bool live = mine < side && t0 + mine < last;
+        const int64_t n = min((int64_t)(t0 + mine) * 16 + c, W.N - 1);
+        f.wc[0] = W.codes + n * (K / 2);
+        f.ws[0] = W.scale + n * (K / 32);
+        f32x4_t acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+        for (int s0 = 0; s0 < steps; s0 += chunk) {
+            const int end = min(s0 + chunk, steps);
+            if (live) f.start(min(s0 + ks, end - 1), by, end);
+            if (!staged || chunk < steps) {
+                __syncthreads();  // the chunk before has been read
+                few_stage(lds, [&](int r) { return X.x + r * X.row_stride; }, M, K, s0, chunk);
+                __syncthreads();
+                staged = true;
+            }
+            if (live) f.run(x, s0 + ks, by, end, s0, acc);
+        }
+        __syncthreads();  // the tiles before have been written
+        sums[wave][lane] = acc[0];
+        __syncthreads();
+        if (wave < side && t0 + wave < last) {
+            f32x4_t v = sums[wave * by][lane];
+            for (int k = 1; k < by; ++k) v += sums[wave * by + k][lane];
+            const int64_t col = (int64_t)(t0 + wave) * 16 + c;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (4 * g + r < M && col < W.N) {
+                    const int64_t at = (4 * g + r) * y_stride + col;
+                    if (y_bf16) static_cast<uint16_t*>(Y)[at] = to_bf16(v[r]);
+                    else static_cast<float*>(Y)[at] = v[r];
+                }
+        }
+    }
+}
+
+static hipError_t launch_few(const Mx4Mat& W, const Mx4X& X, int64_t M, void* Y, bool y_bf16, int64_t y_stride,
+                             hipStream_t st) {
+    const int tiles = (int)((W.N + 15) / 16), steps = (int)((W.K + 127) / 128);
+    int chunk = steps;  // all of X in LDS, or as even pieces as there must be
+    const int room = 144 << 10;
+    if (few_row_bytes(steps) * M > room) {
+        const int most = (int)((room / M - 16) / 256);
+        const int n = (steps + most - 1) / most;
+        chunk = (steps + n - 1) / n;
+    }
+    const int grid = tiles < 256 ? tiles : 256, per = (tiles + grid - 1) / grid;
+    const int side = per < 4 ? per : 4, lds = few_row_bytes(chunk) * (int)M;
+    auto kern = mx4_few_kernel;
+    (void)hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * kFewWaves), lds, st, W, X, (int)M, Y, y_bf16, y_stride, tiles, side,
+                       chunk);
+    return hipGetLastError();
+}
+
+// ---- up to 16 rows of 4 bits: a workgroup of four wavefronts owns 32 rows of W, each every fourth step
+__global__ __launch_bounds__(256) void mx4_few_x4_kernel(Mx4Mat W, Mx4X X, int M, void* __restrict__ Y, int y_bf16,
+                                                         int64_t y_stride) {
+    constexpr int RT = 2, KS = 4, U = 4;
+    __shared__ f32x4_t sums[KS][RT][64];
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+    const int m = min(c, M - 1), groups = (int)W.K / kMxGroup;
+    const uint8_t *xc = X.codes + m * (W.K / 2), *xs = X.scale + m * (W.K / 32);
+    const uint8_t *wc[RT], *ws[RT];
+    f32x4_t acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int64_t n = min(n0 + 16 * t + c, W.N - 1);
+        wc[t] = W.codes + n * (W.K / 2);
+        ws[t] = W.scale + n * (W.K / 32);
+        acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    for (int s = wave; 4 * s < groups; s += U * KS) {
+        u32x4_t w[U][RT], xv[U];  // all loads of U steps first
+        uint32_t sw[U][RT], sx[U];
+        bool in[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = 4 * (s + u * KS) + g, at = min(k, groups - 1);
+            in[u] = k < groups;  // past the end: the last group again, against zeros of X
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                w[u][t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wc[t] + 16 * at));
+                sw[u][t] = ws[t][at];
+            }
+            xv[u] = *reinterpret_cast<const u32x4_t*>(xc + 16 * at);
+            sx[u] = xs[at];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!in[u]) {
+                xv[u] = u32x4_t{0, 0, 0, 0};
+                sx[u] = 0;
+            }
+            const auto wide = [](const u32x4_t& v) { return i32x8_t{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0}; };
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(xv[u]), wide(w[u][t]), acc[t], 4, 4, 0,
+                                                                          (int)sx[u], 0, (int)sw[u][t]);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) sums[wave][t][lane] = acc[t];
+    __syncthreads();
+    if (wave >= RT) return;
+    f32x4_t v = sums[0][wave][lane];
+#pragma unroll
+    for (int k = 1; k < KS; ++k) v += sums[k][wave][lane];
+    const int64_t n = n0 + 16 * wave + c;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (4 * g + r < M && n < W.N) {
+            const int64_t at = (4 * g + r) * y_stride + n;
+            if (y_bf16) static_cast<uint16_t*>(Y)[at] = to_bf16(v[r]);
+            else static_cast<float*>(Y)[at] = v[r];
+        }
 }
 
 // ---- many rows: blocks (mx4_block.hpp), K in `parts` pieces where there are few
@@ -219,9 +373,10 @@ hipError_t launch_mx4_gemm(const Mx4Mat& W, const Mx4X& X, int64_t M, void* Y, b
         const BlockArgs a = {W, X, M, Y, y_stride, y_bf16, 0, 0, p.parts, (float*)work};
         return X.x ? launch_blocks<false>(p.shape, a, st) : launch_blocks<true>(p.shape, a, st);
     }
-    const int64_t tm = (M + 15) / 16, tn = (W.N + 15) / 16;
-    auto kern = X.x ? mx4_gemm_kernel<false> : mx4_gemm_kernel<true>;
-    hipLaunchKernelGGL(kern, dim3((unsigned)(tm * tn)), dim3(64), 0, st, W, X, M, Y, y_bf16, y_stride, (int)tn);
+    if (X.x && M == 1 && W.K <= kGemvMaxK) return launch_gemv1(W, X.x, Y, y_bf16, st);
+    if (X.x) return launch_few(W, X, M, Y, y_bf16, y_stride, st);
+    hipLaunchKernelGGL(mx4_few_x4_kernel, dim3((unsigned)((W.N + 31) / 32)), dim3(256), 0, st, W, X, (int)M, Y, y_bf16,
+                       y_stride);
     return hipGetLastError();
 }
 

@@ -1,148 +1,369 @@
 // The gated FFN of each token's chosen experts, with microscaled 4-bit weights:
 //   y[m] = sum_j weights[m][j] W_down[e] h,  h = bf16(act(W_gate[e] x[m]) * (W_up[e] x[m])),  e = ids[m][j].
 //
-// Pair p = m k + j. The pairs are sorted by expert (mx4_sort_kernel), so that an
-// expert's weights are read once for all of its tokens; the gate/up product writes h in
-// sorted order, the down product each pair's partial row, and the last launch adds up a
-// token's k rows in a fixed order. A pair's place among its expert's is not fixed (it comes
-// from integer atomics), but its results do not depend on it.
-#include "mx4_tile.hpp"
+// Pair p = m k + j. Three ways, by the number of pairs and of pairs an expert gets:
+//   * few pairs (kDirectPairs): each pair's gate and up rows by the one-row kernel, then a token's
+//     y in one pass over its experts' down rows. Two launches, no sorting.
+//   * otherwise the pairs are sorted by expert (mx4_sort_kernel) into tiles of rows of one expert, so
+//     that an expert's weights are read once for a tile; the gate/up product writes h in sorted order,
+//     the down product each pair's part of y (rounded to bf16, as h is), and the last launch
+//     adds up a token's k parts in fp32 and in their order. Tiles of 8 or 16 rows stream
+//     the weights (mx4_few.hpp), tiles of 64 or 128 are blocks on the matrix cores (mx4_block.hpp).
+// A pair's place among its expert's is not fixed (it comes from an integer atomic), but its
+// results do not depend on it.
+#include "mx4_few.hpp"
+#include "mx4_gemv.hpp"
 
 namespace w4 {
 
-constexpr int kMoeTile = 16;  // pairs of one tile
-
 struct Mx4MoeWork {  // byte offsets
-    size_t tiles, pairs, h, part, total;
+    size_t tiles, pairs, place, h, part, total;
     int64_t slots;
 };
+struct MoeWay {
+    bool direct;
+    int rows;  // of a tile
+};
+
+constexpr int64_t kDirectPairs = 16;
+
+static MoeWay moe_way(int64_t M, int k, int64_t E, int64_t D, int64_t F) {
+    const int64_t P = M * k;
+    if (P <= kDirectPairs && k * F <= (32 << 10) && D <= (64 << 10)) return {true, 0};
+    const int64_t each = P / E, room = (144 << 10) / (2 * (D > F ? D : F) + 272);  // rows that fit in LDS
+    if (each <= 6 && room >= 8) return {false, 8};
+    if (each <= 16 && room >= 16) return {false, 16};
+    return {false, each <= 64 ? 64 : 128};
+}
+
 static Mx4MoeWork moe_layout(int64_t M, int k, int64_t E, int64_t D, int64_t F) {
     const int64_t P = M * k;
+    const MoeWay way = moe_way(M, k, E, D, F);
     Mx4MoeWork L;
     const auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
-    L.slots = (E < P ? E : P) + P / kMoeTile;
+    L.slots = way.direct ? 0 : (E + P / way.rows + 7) / 8 * 8;
     L.tiles = 0;
     L.pairs = up((size_t)L.slots * 16);
-    L.h = L.pairs + up((size_t)P * 4);
+    L.place = L.pairs + (way.direct ? 0 : up((size_t)P * 4));
+    L.h = L.place + (way.direct ? 0 : up((size_t)P * 4));
     L.part = L.h + up((size_t)P * F * 2);
-    L.total = L.part + up((size_t)P * D * 4);
+    L.total = L.part + (size_t)P * D * 2;
     return L;
 }
 size_t mx4_moe_workspace(int64_t M, int k, int64_t E, int64_t D, int64_t F) {
     return moe_layout(M, k, E, D, F).total;
 }
 
-// One workgroup: counts, offsets, tiles {expert, first sorted pair, pairs} (-1 past the
-// last) and the sorted pairs. Ids outside [0, E) are no expert's.
-__global__ __launch_bounds__(1024) void mx4_sort_kernel(const int32_t* __restrict__ ids, int64_t P, int E,
-                                                        int64_t slots, int4* __restrict__ tiles,
-                                                        int32_t* __restrict__ pairs) {
-    __shared__ int cnt[1024], off[1024], tile[1024];
-    __shared__ int used;
-    const int t = threadIdx.x;
-    cnt[t] = 0;
+// ---------------------------------------------------------------- few pairs
+constexpr int kDirectWaves = 8;
+
+// h[p][f] of pair blockIdx.y: a gate and an up row a wavefront
+__global__ __launch_bounds__(64 * kDirectWaves) void mx4_gate_up_one_kernel(Mx4Moe a, uint16_t* __restrict__ h) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int p = blockIdx.y, e = a.ids[p], D = (int)a.D;
+    if (e < 0 || e >= a.E) return;
+    const int64_t f = (int64_t)blockIdx.x * kDirectWaves + wave, row = (int64_t)e * a.F + min(f, a.F - 1);
+    GemvStream<2, 1> s;
+    s.groups = D / kMxGroup;
+    s.wc[0] = a.gate.codes + row * (D / 2);
+    s.ws[0] = a.gate.scale + row * (D / 32);
+    s.wc[1] = a.up.codes + row * (D / 2);
+    s.ws[1] = a.up.scale + row * (D / 32);
+    float acc[2] = {0.f, 0.f};
+    s.load(0);
+    gemv_stage(lds, a.x + (p / a.k) * a.x_stride, D);
     __syncthreads();
-    for (int64_t p = t; p < P; p += 1024) {
-        const int e = ids[p];
-        if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+    s.finish(lds, gemv_vectors(D), acc);
+    if (lane == 0 && f < a.F) h[(int64_t)p * a.F + f] = to_bf16(gated(acc[0], acc[1], a.act));
+}
+
+// y[m][d] of token blockIdx.y, a wavefront a d: the rows d of the token's k experts as one row of k F
+// values, against the token's k rows of h, each vector's product times its expert's weight
+__global__ __launch_bounds__(64 * kDirectWaves) void mx4_down_one_kernel(Mx4Moe a, const uint16_t* h) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    __shared__ int ids[32];
+    __shared__ float wts[32];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t m = blockIdx.y;
+    const int F = (int)a.F, G = F / kMxGroup, all = a.k * G, V = gemv_vectors(a.k * F);
+    const int64_t d = (int64_t)blockIdx.x * kDirectWaves + wave, row = min(d, a.D - 1);
+    if ((int)threadIdx.x < a.k) {
+        const int e = a.ids[m * a.k + threadIdx.x];
+        const bool in = e >= 0 && e < a.E;
+        ids[threadIdx.x] = in ? e : -1;
+        wts[threadIdx.x] = in ? a.weights[m * a.k + threadIdx.x] : 0.f;
     }
+    // h of a slot without an expert was never written: its vectors are left out below
+    gemv_stage(lds, h + m * a.k * F, a.k * F);
     __syncthreads();
-    if (t < 64) {  // exclusive sums of counts and tiles, 16 experts a lane
-        int c = 0, n = 0;
-        for (int i = 0; i < 16; ++i) {
-            c += cnt[16 * t + i];
-            n += (cnt[16 * t + i] + kMoeTile - 1) / kMoeTile;
+    float acc = 0.f;
+    constexpr int U = 4;
+    for (int v0 = 0; v0 < V; v0 += 64 * U) {
+        u32x4_t w[U];
+        uint32_t sc[U];
+        float wt[U];
+        bool in[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = min(v0 + 64 * u + lane, all - 1), j = v / G, g = v - j * G, e = ids[j];
+            in[u] = v0 + 64 * u + lane < all && e >= 0;
+            const int64_t at = (int64_t)max(e, 0) * a.D + row;
+            w[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(a.down.codes + at * (F / 2) + 16 * g));
+            sc[u] = a.down.scale[at * (F / 32) + g];
+            wt[u] = wts[j];
         }
-        int ic = c, in = n;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int oc = __shfl_up(ic, d), on = __shfl_up(in, d);
-            if (t >= d) { ic += oc; in += on; }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (v0 + 64 * u >= V) break;
+            const float f = mx4_scale(sc[u]);
+            float dot = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const u32x4_t x = *reinterpret_cast<const u32x4_t*>(lds + j * (16 * V) + (v0 + 64 * u + lane) * 16);
+                const u32x4_t b = __builtin_bit_cast(u32x4_t, mx4_to_bf16(w[u][j], f));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) dot = dot2_bf16(b[q], x[q], dot);
+            }
+            if (in[u]) acc = fmaf(wt[u], dot, acc);
         }
-        int o = ic - c, a = in - n;
-        for (int i = 0; i < 16; ++i) {
-            const int v = cnt[16 * t + i];
-            off[16 * t + i] = o;
-            tile[16 * t + i] = a;
-            o += v;
-            a += (v + kMoeTile - 1) / kMoeTile;
-        }
-        if (t == 63) used = in;
     }
+    acc = group_sum<64>(acc);
+    if (lane == 0 && d < a.D) a.y[m * a.y_stride + d] = to_bf16(acc);
+}
+
+// ---------------------------------------------------------------- sorting
+// Workgroup e: how many pairs lower experts have (o) and how many this one (c), its pairs at sorted places
+// o .. o + c - 1, and its tiles {expert, first place, pairs} at slots from o / rows + e on: one more than
+// its whole tiles at most, so the slots of different experts never meet; unused ones are {-1}.
+// place[p]: the pair's place, -1 for an id outside [0, E).
+__global__ __launch_bounds__(256) void mx4_sort_kernel(const int32_t* __restrict__ ids, int P, int E, int rows, int slots,
+                                                       int4* __restrict__ tiles, int32_t* __restrict__ pairs,
+                                                       int32_t* __restrict__ place) {
+    __shared__ int low[4], same[4], next;
+    const int e = blockIdx.x, t = threadIdx.x;
+    int lo = 0, eq = 0;
+    for (int p = 4 * t; p < P; p += 1024) {
+        if (p + 4 <= P) {
+            const int4 v = *reinterpret_cast<const int4*>(ids + p);
+            lo += (v.x >= 0 && v.x < e) + (v.y >= 0 && v.y < e) + (v.z >= 0 && v.z < e) + (v.w >= 0 && v.w < e);
+            eq += (v.x == e) + (v.y == e) + (v.z == e) + (v.w == e);
+        } else {
+            for (int i = p; i < P; ++i) {
+                lo += ids[i] >= 0 && ids[i] < e;
+                eq += ids[i] == e;
+            }
+        }
+    }
+    for (int o = 32; o >= 1; o >>= 1) {
+        lo += __shfl_xor(lo, o, 64);
+        eq += __shfl_xor(eq, o, 64);
+    }
+    if ((t & 63) == 0) {
+        low[t >> 6] = lo;
+        same[t >> 6] = eq;
+    }
+    if (t == 0) next = 0;
     __syncthreads();
-    if (t < E)
-        for (int i = 0; i * kMoeTile < cnt[t]; ++i)
-            tiles[tile[t] + i] = make_int4(t, off[t] + i * kMoeTile, min(kMoeTile, cnt[t] - i * kMoeTile), 0);
-    for (int64_t s = used + t; s < slots; s += 1024) tiles[s] = make_int4(-1, 0, 0, 0);
-    __syncthreads();
-    for (int64_t p = t; p < P; p += 1024) {
-        const int e = ids[p];
-        if (e >= 0 && e < E) pairs[atomicAdd(&off[e], 1)] = (int)p;
+    const int off = low[0] + low[1] + low[2] + low[3], cnt = same[0] + same[1] + same[2] + same[3];
+    const int base = off / rows + e, end = e + 1 < E ? (off + cnt) / rows + e + 1 : slots;
+    for (int i = base + t; i < end; i += 256) {
+        const int first = (i - base) * rows;
+        tiles[i] = first < cnt ? make_int4(e, off + first, min(rows, cnt - first), 0) : make_int4(-1, 0, 0, 0);
+    }
+    if (cnt == 0 && e > 0) return;  // whole workgroup
+    for (int p = t; p < P; p += 256) {
+        const int v = ids[p];
+        if (v == e) {
+            const int at = off + atomicAdd(&next, 1);
+            pairs[at] = p;
+            place[p] = at;
+        } else if (e == 0 && (v < 0 || v >= E)) {
+            place[p] = -1;
+        }
     }
 }
 
-__global__ __launch_bounds__(64) void mx4_gate_up_kernel(Mx4Moe a, const int4* __restrict__ tiles,
-                                                         const int32_t* __restrict__ pairs,
-                                                         uint16_t* __restrict__ h, int tiles_f) {
-    const int lane = threadIdx.x, g = lane >> 4, c = lane & 15;
-    const int4 t = tiles[blockIdx.x / tiles_f];
+// The tile and the column block of workgroup b: tiles are dealt to the eight XCDs in turn, and a tile's nb
+// column blocks, which share its rows, follow one another on its XCD.
+__device__ __forceinline__ int4 moe_tile(const int4* tiles, int nb, int& block) {
+    const int b = blockIdx.x, i = b / 8;
+    block = i % nb;
+    const int4 t = tiles[i / nb * 8 + b % 8];
+    return make_int4(__builtin_amdgcn_readfirstlane(t.x), __builtin_amdgcn_readfirstlane(t.y),
+                     __builtin_amdgcn_readfirstlane(t.z), 0);
+}
+
+// ---------------------------------------------------------------- tiles of up to 16 rows
+// Wavefront w takes 16 gate rows and the same 16 up rows (or 16 down rows) and all of K.
+template <bool GU, int NW>
+__global__ __launch_bounds__(64 * NW) void mx4_moe_few_kernel(Mx4Moe a, const int4* __restrict__ tiles,
+                                                              const int32_t* __restrict__ pairs, uint16_t* h,
+                                                              uint16_t* __restrict__ part, int nb) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    constexpr int RT = GU ? 2 : 1;
+    int block;
+    const int4 t = moe_tile(tiles, nb, block);
     if (t.x < 0) return;
-    const int64_t f0 = (int64_t)(blockIdx.x % tiles_f) * 16, f = min(f0 + c, a.F - 1);
-    const int64_t row = (int64_t)t.x * a.F + f;
-    const uint16_t* x = a.x + (int64_t)(pairs[t.y + min(c, t.z - 1)] / a.k) * a.x_stride;
-    f32x4_t ag = {0.f, 0.f, 0.f, 0.f}, au = {0.f, 0.f, 0.f, 0.f};
-    mx4_tile_product<false>(x, nullptr, nullptr, a.gate.codes + row * (a.D / 2), a.gate.scale + row * (a.D / 32),
-                            (int)a.D, ag);
-    mx4_tile_product<false>(x, nullptr, nullptr, a.up.codes + row * (a.D / 2), a.up.scale + row * (a.D / 32),
-                            (int)a.D, au);
-    if (f0 + c >= a.F) return;
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t N = GU ? a.F : a.D, n0 = ((int64_t)block * NW + wave) * 16;
+    const int K = (int)(GU ? a.D : a.F), steps = (K + 127) / 128;
+    const int64_t row = (int64_t)t.x * N + min(n0 + c, N - 1);
+    FewStream<RT, GU ? 2 : 3> f;
+    f.groups = K / kMxGroup;
+    f.wc[0] = (GU ? a.gate.codes : a.down.codes) + row * (K / 2);
+    f.ws[0] = (GU ? a.gate.scale : a.down.scale) + row * (K / 32);
+    if constexpr (GU) {
+        f.wc[1] = a.up.codes + row * (K / 2);
+        f.ws[1] = a.up.scale + row * (K / 32);
+    }
+    f32x4_t acc[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    f.start(0, 1, steps);
+    few_stage(lds, [&](int r) { return GU ? a.x + (pairs[t.y + r] / a.k) * a.x_stride : h + (int64_t)(t.y + r) * K; }, t.z, K,
+              0, steps);
+    __syncthreads();
+    if (n0 >= N) return;
+    f.run(lds + min(c, t.z - 1) * few_row_bytes(steps) + 64 * g, 0, 1, steps, 0, acc);
+    if (n0 + c >= N) return;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-        if (4 * g + r < t.z) h[(int64_t)(t.y + 4 * g + r) * a.F + f] = to_bf16(gated(ag[r], au[r], a.act));
+        if (4 * g + r < t.z) {
+            const int64_t at = (int64_t)(t.y + 4 * g + r) * N + n0 + c;
+            if constexpr (GU) h[at] = to_bf16(gated(acc[0][r], acc[1][r], a.act));
+            else part[at] = to_bf16(acc[0][r]);
+        }
 }
 
-__global__ __launch_bounds__(64) void mx4_down_kernel(Mx4Moe a, const int4* __restrict__ tiles,
-                                                      const int32_t* __restrict__ pairs,
-                                                      const uint16_t* __restrict__ h, float* __restrict__ part,
-                                                      int tiles_d) {
-    const int lane = threadIdx.x, g = lane >> 4, c = lane & 15;
-    const int4 t = tiles[blockIdx.x / tiles_d];
+// ---------------------------------------------------------------- blocks
+// A wavefront's columns are pairs of 32 gate and the same 32 up rows, so that it holds both sums of an h.
+template <bool GU, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void mx4_moe_block_kernel(Mx4Moe a, const int4* __restrict__ tiles,
+                                                                        const int32_t* __restrict__ pairs, uint16_t* h,
+                                                                        uint16_t* __restrict__ part, int nb) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    constexpr int NI = BM / WM / 32, NJ = BN / WN / 32, COLS = GU ? BN / 2 : BN;
+    static_assert(NJ == 2, "a gate and an up tile");
+    int block;
+    const int4 t = moe_tile(tiles, nb, block);
     if (t.x < 0) return;
-    const int64_t d0 = (int64_t)(blockIdx.x % tiles_d) * 16, d = min(d0 + c, a.D - 1);
-    const int64_t row = (int64_t)t.x * a.D + d;
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    mx4_tile_product<false>(h + (int64_t)(t.y + min(c, t.z - 1)) * a.F, nullptr, nullptr,
-                            a.down.codes + row * (a.F / 2), a.down.scale + row * (a.F / 32), (int)a.F, acc);
-    if (d0 + c >= a.D) return;
+    const int64_t N = GU ? a.F : a.D, n0 = (int64_t)block * COLS;
+    const int K = (int)(GU ? a.D : a.F);
+    f32x16_t acc[NI][NJ];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-        if (4 * g + r < t.z) part[(int64_t)pairs[t.y + 4 * g + r] * a.D + d] = acc[r];
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16_t{};
+    const auto xrow = [&](int r) -> const uint16_t* {
+        const int p = t.y + min(r, t.z - 1);
+        return GU ? a.x + (pairs[p] / a.k) * a.x_stride : h + (int64_t)p * K;
+    };
+    const auto wcol = [&](int c) {
+        const Mx4Mat& w = !GU ? a.down : (c / 32) & 1 ? a.up : a.gate;
+        const int64_t n = (int64_t)t.x * N + min(n0 + (GU ? c / 64 * 32 + c % 32 : c), N - 1);
+        return Mx4Mat{w.codes + n * (K / 2), w.scale + n * (K / 32), 0, 0};
+    };
+    mx4_block_product<BM, BN, WM, WN>(lds, xrow, wcol, K, 0, (K + kBlockK - 1) / kBlockK, acc);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int row = (wave / WN) * (BM / WM) + 4 * (lane >> 5);
+    const int64_t n = n0 + (wave % WN) * (GU ? 32 : 64) + (lane & 31);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int m = row + 32 * i + 8 * (r >> 2) + (r & 3);
+            if (m >= t.z) continue;
+            const int64_t at = (int64_t)(t.y + m) * N + n;
+            if constexpr (GU) {
+                if (n < N) h[at] = to_bf16(gated(acc[i][0][r], acc[i][1][r], a.act));
+            } else {
+                if (n < N) part[at] = to_bf16(acc[i][0][r]);
+                if (n + 32 < N) part[at + 32] = to_bf16(acc[i][1][r]);
+            }
+        }
 }
 
-__global__ __launch_bounds__(256) void mx4_combine_kernel(Mx4Moe a, const float* __restrict__ part) {
+// ---------------------------------------------------------------- a token's parts
+__global__ __launch_bounds__(256) void mx4_combine_kernel(Mx4Moe a, const int32_t* __restrict__ place,
+                                                          const uint16_t* __restrict__ part) {
     const int64_t m = blockIdx.x;
-    for (int64_t d = threadIdx.x; d < a.D; d += 256) {
-        float y = 0.f;
+    for (int64_t d = 8 * threadIdx.x; d < a.D; d += 8 * 256) {
+        float y[8] = {};
         for (int j = 0; j < a.k; ++j) {
-            const int e = a.ids[m * a.k + j];
-            if (e >= 0 && e < a.E) y = fmaf(a.weights[m * a.k + j], part[(m * a.k + j) * a.D + d], y);
+            const int p = place[m * a.k + j];
+            if (p < 0) continue;
+            const float w = a.weights[m * a.k + j];
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(part + (int64_t)p * a.D + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[2 * i] = fmaf(w, __uint_as_float(v[i] << 16), y[2 * i]);
+                y[2 * i + 1] = fmaf(w, __uint_as_float(v[i] & 0xFFFF0000u), y[2 * i + 1]);
+            }
         }
-        a.y[m * a.y_stride + d] = to_bf16(y);
+        uint16_t* out = a.y + m * a.y_stride + d;
+        if ((a.y_stride & 7) == 0) {
+            bf16x8_t o;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = (__bf16)y[i];
+            *reinterpret_cast<bf16x8_t*>(out) = o;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) out[i] = to_bf16(y[i]);
+        }
     }
+}
+
+template <int BM, int BN, int WM, int WN>
+static void launch_moe_blocks(const Mx4Moe& a, int64_t slots, const int4* tiles, const int32_t* pairs, uint16_t* h,
+                              uint16_t* part, hipStream_t st) {
+    const int lds = kStages * mx4_stage_bytes<BM, BN>(), nf = (int)((a.F + BN / 2 - 1) / (BN / 2)), nd = (int)((a.D + BN - 1) / BN);
+    auto gu = mx4_moe_block_kernel<true, BM, BN, WM, WN>;
+    auto down = mx4_moe_block_kernel<false, BM, BN, WM, WN>;
+    (void)hipFuncSetAttribute((const void*)gu, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    (void)hipFuncSetAttribute((const void*)down, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    hipLaunchKernelGGL(gu, dim3((unsigned)(slots * nf)), dim3(64 * WM * WN), lds, st, a, tiles, pairs, h, part, nf);
+    hipLaunchKernelGGL(down, dim3((unsigned)(slots * nd)), dim3(64 * WM * WN), lds, st, a, tiles, pairs, h, part, nd);
 }
 
 hipError_t launch_mx4_moe(const Mx4Moe& a, void* work, hipStream_t st) {
     const Mx4MoeWork L = moe_layout(a.M, a.k, a.E, a.D, a.F);
+    const MoeWay way = moe_way(a.M, a.k, a.E, a.D, a.F);
+    if (L.slots * ((a.D > a.F ? a.D : a.F) / 64 + 1) > 0x7fffffff) return hipErrorInvalidValue;
     uint8_t* base = (uint8_t*)work;
     int4* tiles = (int4*)(base + L.tiles);
     int32_t* pairs = (int32_t*)(base + L.pairs);
+    int32_t* place = (int32_t*)(base + L.place);
     uint16_t* h = (uint16_t*)(base + L.h);
-    float* part = (float*)(base + L.part);
-    const int tf = (int)((a.F + 15) / 16), td = (int)((a.D + 15) / 16);
-    hipLaunchKernelGGL(mx4_sort_kernel, dim3(1), dim3(1024), 0, st, a.ids, a.M * a.k, a.E, L.slots, tiles, pairs);
-    hipLaunchKernelGGL(mx4_gate_up_kernel, dim3((unsigned)(L.slots * tf)), dim3(64), 0, st, a, tiles, pairs, h, tf);
-    hipLaunchKernelGGL(mx4_down_kernel, dim3((unsigned)(L.slots * td)), dim3(64), 0, st, a, tiles, pairs, h, part,
-                       td);
-    hipLaunchKernelGGL(mx4_combine_kernel, dim3((unsigned)a.M), dim3(256), 0, st, a, part);
+    uint16_t* part = (uint16_t*)(base + L.part);
+    if (way.direct) {
+        const dim3 gu((unsigned)((a.F + kDirectWaves - 1) / kDirectWaves), (unsigned)(a.M * a.k));
+        const dim3 gd((unsigned)((a.D + kDirectWaves - 1) / kDirectWaves), (unsigned)a.M);
+        const int lds = gemv_lds_bytes((int)a.D);
+        (void)hipFuncSetAttribute((const void*)mx4_gate_up_one_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        hipLaunchKernelGGL(mx4_gate_up_one_kernel, gu, dim3(64 * kDirectWaves), lds, st, a, h);
+        hipLaunchKernelGGL(mx4_down_one_kernel, gd, dim3(64 * kDirectWaves), gemv_lds_bytes((int)(a.k * a.F)), st, a, h);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(mx4_sort_kernel, dim3((unsigned)a.E), dim3(256), 0, st, a.ids, (int)(a.M * a.k), a.E, way.rows,
+                       (int)L.slots, tiles, pairs, place);
+    if (way.rows <= 16) {
+        constexpr int GW = 4, DW = 8;
+        const int nf = (int)((a.F + 16 * GW - 1) / (16 * GW)), nd = (int)((a.D + 16 * DW - 1) / (16 * DW));
+        const int lg = way.rows * few_row_bytes((int)(a.D + 127) / 128), ld = way.rows * few_row_bytes((int)(a.F + 127) / 128);
+        auto gu = mx4_moe_few_kernel<true, GW>;
+        auto down = mx4_moe_few_kernel<false, DW>;
+        (void)hipFuncSetAttribute((const void*)gu, hipFuncAttributeMaxDynamicSharedMemorySize, lg);
+        (void)hipFuncSetAttribute((const void*)down, hipFuncAttributeMaxDynamicSharedMemorySize, ld);
+        hipLaunchKernelGGL(gu, dim3((unsigned)(L.slots * nf)), dim3(64 * GW), lg, st, a, tiles, pairs, h, part, nf);
+        hipLaunchKernelGGL(down, dim3((unsigned)(L.slots * nd)), dim3(64 * DW), ld, st, a, tiles, pairs, h, part, nd);
+    } else if (way.rows == 64) {
+        launch_moe_blocks<64, 256, 1, 4>(a, L.slots, tiles, pairs, h, part, st);
+    } else {
+        launch_moe_blocks<128, 128, 2, 2>(a, L.slots, tiles, pairs, h, part, st);
+    }
+    hipLaunchKernelGGL(mx4_combine_kernel, dim3((unsigned)a.M), dim3(256), 0, st, a, place, part);
     return hipGetLastError();
 }
 
