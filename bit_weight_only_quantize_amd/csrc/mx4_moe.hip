@@ -137,23 +137,25 @@ __global__ __launch_bounds__(64 * kDirectWaves) void mx4_down_one_kernel(Mx4Moe 
 // o .. o + c - 1, and its tiles {expert, first place, pairs} at slots from o / rows + e on: one more than
 // its whole tiles at most, so the slots of different experts never meet; unused ones are {-1}.
 // place[p]: the pair's place, -1 for an id outside [0, E).
-__global__ __launch_bounds__(256) void mx4_sort_kernel(const int32_t* __restrict__ ids, int P, int E, int rows, int slots,
-                                                       int4* __restrict__ tiles, int32_t* __restrict__ pairs,
-                                                       int32_t* __restrict__ place) {
-    __shared__ int low[4], same[4], next;
+constexpr int kSortThreads = 1024;
+__global__ __launch_bounds__(kSortThreads) void mx4_sort_kernel(const int32_t* __restrict__ ids, int P, int E, int rows,
+                                                                int slots, int4* __restrict__ tiles,
+                                                                int32_t* __restrict__ pairs, int32_t* __restrict__ place) {
+    __shared__ int low[kSortThreads / 64], same[kSortThreads / 64], next;
     const int e = blockIdx.x, t = threadIdx.x;
+    const auto four = [&](int p) {  // ids p .. p + 3; behind the last, one that is no expert's and has no place
+        if (p + 4 <= P) return *reinterpret_cast<const int4*>(ids + p);
+        int4 v = {INT32_MIN, INT32_MIN, INT32_MIN, INT32_MIN};
+        if (p < P) v.x = ids[p];
+        if (p + 1 < P) v.y = ids[p + 1];
+        if (p + 2 < P) v.z = ids[p + 2];
+        return v;
+    };
     int lo = 0, eq = 0;
-    for (int p = 4 * t; p < P; p += 1024) {
-        if (p + 4 <= P) {
-            const int4 v = *reinterpret_cast<const int4*>(ids + p);
-            lo += (v.x >= 0 && v.x < e) + (v.y >= 0 && v.y < e) + (v.z >= 0 && v.z < e) + (v.w >= 0 && v.w < e);
-            eq += (v.x == e) + (v.y == e) + (v.z == e) + (v.w == e);
-        } else {
-            for (int i = p; i < P; ++i) {
-                lo += ids[i] >= 0 && ids[i] < e;
-                eq += ids[i] == e;
-            }
-        }
+    for (int p = 4 * t; p < P; p += 4 * kSortThreads) {
+        const int4 v = four(p);
+        lo += (v.x >= 0 && v.x < e) + (v.y >= 0 && v.y < e) + (v.z >= 0 && v.z < e) + (v.w >= 0 && v.w < e);
+        eq += (v.x == e) + (v.y == e) + (v.z == e) + (v.w == e);
     }
     for (int o = 32; o >= 1; o >>= 1) {
         lo += __shfl_xor(lo, o, 64);
@@ -165,22 +167,33 @@ __global__ __launch_bounds__(256) void mx4_sort_kernel(const int32_t* __restrict
     }
     if (t == 0) next = 0;
     __syncthreads();
-    const int off = low[0] + low[1] + low[2] + low[3], cnt = same[0] + same[1] + same[2] + same[3];
+    int off = 0, cnt = 0;
+#pragma unroll
+    for (int i = 0; i < kSortThreads / 64; ++i) {
+        off += low[i];
+        cnt += same[i];
+    }
     const int base = off / rows + e, end = e + 1 < E ? (off + cnt) / rows + e + 1 : slots;
-    for (int i = base + t; i < end; i += 256) {
+    for (int i = base + t; i < end; i += kSortThreads) {
         const int first = (i - base) * rows;
         tiles[i] = first < cnt ? make_int4(e, off + first, min(rows, cnt - first), 0) : make_int4(-1, 0, 0, 0);
     }
     if (cnt == 0 && e > 0) return;  // whole workgroup
-    for (int p = t; p < P; p += 256) {
-        const int v = ids[p];
+    const auto put = [&](int p, int v) {
         if (v == e) {
             const int at = off + atomicAdd(&next, 1);
             pairs[at] = p;
             place[p] = at;
-        } else if (e == 0 && (v < 0 || v >= E)) {
+        } else if (e == 0 && p < P && (v < 0 || v >= E)) {
             place[p] = -1;
         }
+    };
+    for (int p = 4 * t; p < P; p += 4 * kSortThreads) {
+        const int4 v = four(p);
+        put(p, v.x);
+        put(p + 1, v.y);
+        put(p + 2, v.z);
+        put(p + 3, v.w);
     }
 }
 
@@ -346,7 +359,7 @@ hipError_t launch_mx4_moe(const Mx4Moe& a, void* work, hipStream_t st) {
         hipLaunchKernelGGL(mx4_down_one_kernel, gd, dim3(64 * kDirectWaves), gemv_lds_bytes((int)(a.k * a.F)), st, a, h);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL(mx4_sort_kernel, dim3((unsigned)a.E), dim3(256), 0, st, a.ids, (int)(a.M * a.k), a.E, way.rows,
+    hipLaunchKernelGGL(mx4_sort_kernel, dim3((unsigned)a.E), dim3(kSortThreads), 0, st, a.ids, (int)(a.M * a.k), a.E, way.rows,
                        (int)L.slots, tiles, pairs, place);
     if (way.rows <= 16) {
         constexpr int GW = 4, DW = 8;

@@ -1,9 +1,15 @@
 // Selection of experts from router logits.
 //
-// Scores s = softmax(l) or sigmoid(l), choice values c = s + bias. Scores lie close
-// together (two of 256 experts' values are within a unit in the last place of fp32 about once in
-// ten thousand tokens), so choices are made in 64 bits; without a bias they are made on the
-// logits themselves, whose order the scores have.
+// Scores s = softmax(l) or sigmoid(l), choice values c = s + bias. Values lie close together (two of
+// 256 experts' are within a unit in the last place of fp32 of each other about once in ten
+// thousand tokens), and choices are those of 64-bit arithmetic. A wavefront takes a token:
+//   * Without a bias the choice is made on the logits, exactly; group values of one expert too.
+//   * Otherwise values are computed in fp32, with a bound on their errors, and every
+//     decision (each chosen expert against the next, kept groups against the best other one) has to
+//     have a margin beyond it. A token without (ties, mostly) is done again in 64 bits.
+// Sorting is k rounds of a wave-wide maximum over 32-bit keys; a lane holds consecutive experts, so the
+// first lane with the maximum has the lowest index. Bound by instruction issue: 8192 tokens, 256 experts in
+// 8 groups, top 8, sigmoid with bias: TBD us (27 with everything in 64 bits; 1.7 for the bytes).
 #include "mx4.hpp"
 #include "topk.hpp"
 
@@ -16,6 +22,11 @@ __device__ __forceinline__ uint64_t order_key(double v) {
     const int64_t b = __double_as_longlong(v + 0.0);  // -0 counts as 0
     return b < 0 ? ~(uint64_t)b : (uint64_t)b | (1ull << 63);
 }
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const int32_t b = __float_as_int(v + 0.f);
+    return b < 0 ? ~(uint32_t)b : (uint32_t)b | (1u << 31);
+}
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k); }
 
 __device__ __forceinline__ uint32_t wave_max_u(uint32_t v) {
     return (uint32_t)wave_reduce_i((int)v, [](int a, int b) { return (uint32_t)a > (uint32_t)b ? a : b; });
@@ -30,27 +41,26 @@ __device__ __forceinline__ double wave_sum_d(double v) {
     return v;
 }
 
-// One wavefront a token; lane holds the experts lane + 64 j.
+template <bool BF16>
+__device__ __forceinline__ float logit(const SelectArgs& a, int64_t m, int e) {
+    const int64_t at = m * a.row_stride + e;
+    return BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
+}
+
+// A token with everything in 64 bits; lane holds the experts lane + 64 j. values: [1024] in LDS.
 template <int EPL, bool BF16>
-__global__ __launch_bounds__(64) void moe_select_kernel(SelectArgs a) {
+__device__ void select_exact(const SelectArgs& a, int64_t m, double* values) {
     const int lane = threadIdx.x;
-    const int64_t m = blockIdx.x;
-    __shared__ double gval[1024];
     float l[EPL];
     float mx = -INFINITY;
-    bool nan = false;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         const int e = lane + 64 * j;
-        const int64_t at = m * a.row_stride + min(e, a.E - 1);
-        const float v = BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(a.logits)[at])
-                             : static_cast<const float*>(a.logits)[at];
+        const float v = logit<BF16>(a, m, min(e, a.E - 1));
         l[j] = e < a.E ? v : -INFINITY;
-        nan |= e < a.E && v != v;
         mx = fmaxf(mx, l[j]);
     }
     mx = wave_max_dpp(mx);
-    nan = __any(nan);
     double p[EPL];
     double sum = 0;
 #pragma unroll
@@ -77,14 +87,14 @@ __global__ __launch_bounds__(64) void moe_select_kernel(SelectArgs a) {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const int e = lane + 64 * j;
-            if (e < a.E) gval[e] = !(l[j] > -INFINITY) ? -INFINITY : p[j] + (a.bias ? (double)a.bias[e] : 0.0);
+            if (e < a.E) values[e] = !(l[j] > -INFINITY) ? -INFINITY : p[j] + (a.bias ? (double)a.bias[e] : 0.0);
         }
         __syncthreads();
         double v = 0;
         if (lane < a.groups) {
             double b0 = -INFINITY, b1 = -INFINITY;
             for (int i = 0; i < size; ++i) {
-                const double x = gval[lane * size + i];
+                const double x = values[lane * size + i];
                 if (x > b0) { b1 = b0; b0 = x; }
                 else if (x > b1) b1 = x;
             }
@@ -133,7 +143,166 @@ __global__ __launch_bounds__(64) void moe_select_kernel(SelectArgs a) {
     if (lane < a.k) {
         if (a.renormalize) w = total > 0 ? w / total : 0.0;
         a.ids[m * a.k + lane] = id;
-        a.weights[m * a.k + lane] = nan ? NAN : (float)(w * (double)a.scale);
+        a.weights[m * a.k + lane] = (float)(w * (double)a.scale);
+    }
+}
+
+// Errors of the fp32 values. exp2 of y = (l - max) log2 e: y is off by 2^-23 |y|, its power by that times itself and a
+// unit, 2^y (|y| 2^-23 + 2^-23) <= 2^-22; the sum of up to 16 + 6 additions by 22 * 2^-24 of itself: a softmax is
+// within 2^-19 / sum of the true one, its largest. A sigmoid s has s (1 - s) times the power's
+// relative error, and units for the sum and the reciprocal: within 2^-21. c's rounding: 2^-24 |c|.
+constexpr float kSoftmaxOff = 0x1p-19f, kSigmoidOff = 0x1p-21f;
+
+template <int EPL, bool BF16>
+__global__ __launch_bounds__(64) void moe_select_kernel(SelectArgs a) {
+    __shared__ double values[1024];
+    const int lane = threadIdx.x;
+    const int64_t m = blockIdx.x;
+    float l[EPL], c[EPL];
+    float mx = -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        const int e = lane * EPL + j;
+        const float v = logit<BF16>(a, m, min(e, a.E - 1));
+        l[j] = e < a.E ? v : -INFINITY;
+        nan |= e < a.E && v != v;
+        mx = fmaxf(mx, l[j]);
+    }
+    if (__any(nan)) {  // NaN experts are masked, and every weight is NaN
+        select_exact<EPL, BF16>(a, m, values);
+        if (lane < a.k) a.weights[m * a.k + lane] = NAN;
+        return;
+    }
+    const bool grouped = a.groups > 1, by_logit = !a.bias;
+    const bool need_sum = !a.sigmoid, need_scores = a.bias || (grouped && a.best == 2);
+    float inv = 1.f, off = kSigmoidOff;
+    if (need_sum) {
+        mx = wave_max_dpp(mx);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            c[j] = __builtin_amdgcn_exp2f(1.4426950408889634f * (l[j] - mx));  // -infinity gives 0
+            sum += c[j];
+        }
+        sum = wave_sum_dpp(sum);
+        inv = mx > -INFINITY ? 1.f / sum : 0.f;
+        off = kSoftmaxOff * inv;
+    }
+    if (need_scores) {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const float s = a.sigmoid ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * l[j])) : c[j] * inv;
+            const int e = lane * EPL + j;
+            c[j] = !(l[j] > -INFINITY) ? -INFINITY : a.bias && e < a.E ? s + a.bias[e] : s;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) c[j] = l[j];
+    }
+    bool close = false;  // some decision is within the errors; an infinite or NaN c compares so too
+    uint64_t kept = ~0ull;
+    const int size = a.E / a.groups;
+    if (grouped) {
+        // `share` lanes (a power of two) scan a group, then merge their two largest
+        float* vals = reinterpret_cast<float*>(values);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const int e = lane * EPL + j;
+            if (e < a.E) vals[e] = c[j];
+        }
+        __syncthreads();
+        int share = 1;
+        while (2 * share * a.groups <= 64) share *= 2;
+        const int g = lane / share;
+        float b0 = -INFINITY, b1 = -INFINITY, big = 0.f;
+        if (g < a.groups)
+            for (int i = lane & (share - 1); i < size; i += share) {
+                const float x = vals[g * size + i];
+                b1 = fmaxf(b1, fminf(b0, x));
+                b0 = fmaxf(b0, x);
+            }
+        for (int o = 1; o < share; o *= 2) {
+            const float o0 = __shfl_xor(b0, o, 64), o1 = __shfl_xor(b1, o, 64);
+            b1 = fmaxf(fmaxf(b1, o1), fminf(b0, o0));
+            b0 = fmaxf(b0, o0);
+        }
+        const float v = a.best == 2 ? b0 + b1 : b0;
+        if (need_scores) {
+            big = b0 > -INFINITY ? fabsf(b0) : 0.f;
+            if (a.best == 2 && b1 > -INFINITY) big = fmaxf(big, fabsf(b1));
+            big = wave_max_dpp(big);
+            close |= v != v;
+        }
+        // (lane & (share - 1)) == 0 speaks for group g
+        uint32_t gk = (lane & (share - 1)) == 0 && g < a.groups ? (v > -INFINITY ? order_key(v) : 1u) : 0u;
+        uint32_t last = 0;
+        kept = 0;
+        for (int r = 0; r < a.top_groups; ++r) {
+            last = wave_max_u(gk);
+            const int at = __ffsll((unsigned long long)__ballot(gk == last)) - 1;
+            kept |= 1ull << (at / share);
+            if (lane == at) gk = 0;
+        }
+        const uint32_t next = wave_max_u(gk);
+        if (next > 1 && last > 1) {
+            const float p = key_value(last), q = key_value(next);
+            if (need_scores) close |= !(p - q > 4.f * off + 0x1p-21f * big);
+            // logits of the best experts order their scores; but where scores saturate in 64 bits, or
+            // logits differ by next to nothing, equal scores of different logits are a tie
+            else close |= p != q && (p - q < 0x1p-30f || q < (a.sigmoid ? -600.f : mx - 600.f) || (a.sigmoid && q > 16.f));
+        }
+    }
+    uint32_t key[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        const int e = lane * EPL + j;
+        const float v = by_logit ? l[j] : c[j];
+        const bool can = e < a.E && (!grouped || ((kept >> (e / size)) & 1));
+        if (!by_logit) close |= v != v;
+        key[j] = !can ? 0u : l[j] > -INFINITY ? order_key(v) : 1u;
+    }
+    int id = 0;
+    uint32_t prev = 0;
+    for (int r = 0; r <= a.k; ++r) {
+        uint32_t b = key[0];
+#pragma unroll
+        for (int j = 1; j < EPL; ++j) b = max(b, key[j]);
+        const uint32_t best = wave_max_u(b);
+        if (!by_logit && r > 0 && prev > 1 && best > 1) {
+            const float p = key_value(prev), q = key_value(best);
+            close |= !(p - q > 2.f * off + 0x1p-22f * fmaxf(fabsf(p), fabsf(q)));
+        }
+        prev = best;
+        if (r == a.k) break;
+        const int at = __ffsll((unsigned long long)__ballot(b == best)) - 1;
+        int j = 0;
+#pragma unroll
+        for (int i = EPL - 1; i >= 0; --i) j = key[i] == best ? i : j;
+        j = __builtin_amdgcn_readlane(j, at);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (lane == at && i == j) key[i] = 0;
+        if (lane == r) id = at * EPL + j;
+    }
+    if (__any(close)) {
+        select_exact<EPL, BF16>(a, m, values);
+        return;
+    }
+    // the chosen experts' scores in 64 bits, each by its lane
+    double w = 0, total = 0;
+    if (lane < a.k) {
+        const float x = logit<BF16>(a, m, id);
+        if (x > -INFINITY) w = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)mx) * (double)inv;
+    }
+    if (a.renormalize) {
+        total = w;
+        for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor(total, o, 64);  // k <= 32 lanes
+        w = total > 0 ? w / total : 0.0;
+    }
+    if (lane < a.k) {
+        a.ids[m * a.k + lane] = id;
+        a.weights[m * a.k + lane] = (float)(w * (double)a.scale);
     }
 }
 
@@ -145,6 +314,7 @@ hipError_t launch_moe_select(const SelectArgs& a, bool bf16, hipStream_t st) {
         else hipLaunchKernelGGL((moe_select_kernel<EPL, false>), grid, block, 0, st, a);                 \
         return hipGetLastError();                                                                        \
     }
+    W4_SELECT(1)
     W4_SELECT(2)
     W4_SELECT(4)
     W4_SELECT(16)
