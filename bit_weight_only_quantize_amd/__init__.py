@@ -684,17 +684,19 @@ def kv_attention(q: torch.Tensor, cache: KVPages, batch: KVBatch, scale: Optiona
 # ---------------------------------------------------------------- microscaled 4-bit
 def _mx4_rows(t: torch.Tensor, name: str, rows: Optional[int], width: Optional[int], types=_ROW_TYPES) -> _W4Rows:
     """w4_rows of a device tensor [rows][width], contiguous along its rows."""
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (width is not None and t.shape[1] != width):
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (width is not None and shape[1] != width):
         raise ValueError(f"{name} must be [{'rows' if rows is None else rows}][{'columns' if width is None else width}],"
-                         f" not {tuple(t.shape)}")
+                         f" not {tuple(shape)}")
     code = types.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be {' or '.join(str(d).split('.')[1] for d in types)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] > 1:
         raise ValueError(f"{name} must be contiguous along its rows")
-    return _W4Rows(t.data_ptr(), code, t.stride(0), 0)
+    return _W4Rows(t.data_ptr(), code, s0)
 
 
 _BF16_ROWS = {torch.bfloat16: 1}
@@ -704,26 +706,28 @@ def _mx4_matrix(q: QuantizedMatrix, name: str, index: Optional[int] = None) -> _
     """The descriptor of a microscaled matrix, its tensors checked against its sizes."""
     if q.scheme != "mx4_g32":
         raise ValueError(f"{name} is {q.scheme}, not mx4_g32")
-    c, s = q.codes, q.scale
-    if c.dtype != torch.uint8 or s.dtype != torch.uint8 or not c.is_cuda or not s.is_cuda \
-            or not c.is_contiguous() or not s.is_contiguous():
+    c, s, E, N, K = q.codes, q.scale, q.num_experts, q.N, q.K
+    if c.dtype is not torch.uint8 or s.dtype is not torch.uint8 or not c.is_contiguous() or not s.is_contiguous():
         raise ValueError(f"{name}: codes and scale must be contiguous uint8 device tensors")
-    n = q.num_experts * q.N
-    if 2 * c.numel() != n * q.K or 32 * s.numel() != n * q.K:
-        raise ValueError(f"{name}: codes {tuple(c.shape)} and scale {tuple(s.shape)} for {q.num_experts} x [{q.N}][{q.K}]")
-    d = c.get_device()
-    if s.get_device() != d or (index is not None and d != index):
-        raise ValueError(f"{name} is on more than one device, or on another one")
-    return q.desc()
+    n = E * N * K
+    if 2 * c.numel() != n or 32 * s.numel() != n:
+        raise ValueError(f"{name}: codes {tuple(c.shape)} and scale {tuple(s.shape)} for {E} x [{N}][{K}]")
+    d = c.get_device()                               # -1 on the host
+    if d < 0 or s.get_device() != d or (index is not None and d != index):
+        raise ValueError(f"{name} is not on the device of the call")
+    return _W4Matrix(3, E, N, K, c.data_ptr(), s.data_ptr())
+
+
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _on(index: int, f, *args) -> None:
     """f(*args, stream) on device `index` and its current stream."""
-    if torch.cuda.current_device() == index:
-        rc = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    if _device() == index:
+        rc = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            rc = f(*args, torch._C._cuda_getCurrentRawStream(index))
+            rc = f(*args, _raw_stream(index))
     if rc:
         _check(rc)
 
@@ -745,7 +749,7 @@ def mx4_quantize(x: torch.Tensor, out: Optional[QuantizedMatrix] = None) -> Quan
         raise ValueError(f"out is {out.num_experts} x [{out.N}][{out.K}], x [{rows}][{K}]")
     index = x.get_device()
     _mx4_matrix(out, "out", index)
-    _on(index, lib().w4_mx4_quantize, d, rows, K, _ptr(out.codes), _ptr(out.scale))
+    _on(index, lib().w4_mx4_quantize, d, rows, K, out.codes.data_ptr(), out.scale.data_ptr())
     return out
 
 

@@ -48,6 +48,21 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
     return (act == kActSilu ? g / (1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g)) : gelu_tanh(g)) * u;
 }
 
+// More dynamic LDS than the default 64 KiB for a kernel, up to `most`; asked for once on each device.
+constexpr int kMostLds = 144 << 10;  // beside static arrays of up to 16 KiB
+template <typename F>
+inline hipError_t allow_lds(F* kern, int bytes, int most, uint64_t* asked) {
+    if (bytes <= (64 << 10)) return hipSuccess;
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (__atomic_load_n(asked, __ATOMIC_RELAXED) & bit)) return hipSuccess;
+    e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == hipSuccess && dev < 64) __atomic_fetch_or(asked, bit, __ATOMIC_RELAXED);
+    return e;
+}
+
 // ---- rows <-> codes (mx4_rows.hip)
 hipError_t launch_mx4_quantize(const void* x, bool bf16, int64_t row_stride, int64_t rows, int64_t K,
                                uint8_t* codes, uint8_t* scale, hipStream_t st);

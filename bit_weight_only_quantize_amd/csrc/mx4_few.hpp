@@ -1,81 +1,118 @@
 // Products with microscaled 4-bit weights for few rows (one tile of 16): the weights are
 // streamed from memory to registers once, so the work is laid out for loads in flight.
 //
-// Sixteen code bytes are one group of 32 k: lane 16g + c loads those of group 4s + g of row c of W
-// in step s of 128 k, converts them (exact, one instruction for two weights) and multiplies word j
-// of them with the same k of row c of X in matrix instruction j of v_mfma_f32_16x16x32_bf16, so
-// weights go from memory to the matrix cores with no exchange between lanes.
-//   * X waits in LDS, zeros behind K: operands of X are four times the codes they meet, and
-//     as lane loads from the caches they were what bounded the kernel (13 rows, 5120 -> 13824: 25 us against 18.5). Rows are 16 bytes off a multiple of 256, so that
-//     sixteen rows' operands lie in different banks.
-//   * A wavefront keeps DEPTH steps of codes in flight and starts them before X is staged.
-//   * Rows of X in 4 bits need no conversion and no LDS: one v_mfma_scale_f32_16x16x128_f8f6f4 a
-//     step on the codes of both sides as stored.
+// Sixteen code bytes are one group of 32 k. A load takes 128 consecutive bytes (eight groups, a whole
+// cache line) of eight rows of W: lane 16g + c group 4 (c % 2) + g of row c / 2. (64 bytes of 16 rows, the
+// plain layout of a matrix operand, reach 3.2 TB/s instead of 4.3 on a long stream.) Column c of a
+// 16-column operand is then half c % 2 of row c / 2, and meets both halves of X in two products, of which
+// the even columns of one and the odd ones of the other are kept; neighbouring lanes add theirs up
+// at the end. Codes become bf16 exactly, one instruction for two weights, and go to
+// v_mfma_f32_16x16x32_bf16 word by word, with no exchange between lanes before.
+//   * X waits in LDS, zeros behind K: as lane loads from the caches its operands, four times the codes they
+//     meet, were what bounded the kernel. Rows are 16 bytes off a multiple of 256, so that sixteen
+//     rows' operands lie in different banks.
+//   * A wavefront starts its first step of codes before X is staged, and the next one once a step is used up: with
+//     16 or more wavefronts a CU more loads in flight made every kernel here slower.
 #pragma once
 
 #include "mx4_block_x4.hpp"
 
 namespace w4 {
 
-// bytes of one row of X of `steps` steps in LDS
-__host__ __device__ inline int few_row_bytes(int steps) { return 256 * steps + 16; }
+constexpr int kFewK = 256;  // k of a step
 
-// Stages k [128 s0, 128 (s0 + steps)) of `rows` rows, by all threads of the workgroup. row(r): the row's values.
+// bytes of one row of X of `steps` steps in LDS
+__host__ __device__ inline int few_row_bytes(int steps) { return 2 * kFewK * steps + 16; }
+__host__ __device__ inline int few_steps(int64_t K) { return (int)((K + kFewK - 1) / kFewK); }
+
+// Stages steps s0 .. s0 + steps - 1 of `rows` rows, by all threads of the workgroup. row(r): the row's values.
 template <typename Row>
 __device__ __forceinline__ void few_stage(uint8_t* lds, Row row, int rows, int K, int s0, int steps) {
-    const int per = 16 * steps, stride = few_row_bytes(steps);
+    const int per = kFewK / 8 * steps, stride = few_row_bytes(steps);
     for (int v = threadIdx.x; v < rows * per; v += blockDim.x) {
-        const int r = v / per, i = v - r * per, k = 128 * s0 + 8 * i;
+        const int r = v / per, i = v - r * per, k = kFewK * s0 + 8 * i;
         u32x4_t x = {0, 0, 0, 0};
         if (k < K) x = *reinterpret_cast<const u32x4_t*>(row(r) + k);
         *reinterpret_cast<u32x4_t*>(lds + r * stride + 16 * i) = x;
     }
 }
 
-// The wavefront's steps s = first, first + by, ... < end, over X staged from step s0 on: acc[t][r] +=
-// X[4g + r] . W_t[c]. wc[t], ws[t]: row c's codes and scales.
-template <int RT, int DEPTH>
-struct FewStream {
-    u32x4_t w[DEPTH][RT];
-    uint32_t sc[DEPTH][RT];
-    const uint8_t *wc[RT], *ws[RT];
-    int groups;
-    __device__ __forceinline__ void load(int u, int s) {  // past the end: the last group (against zeros of X)
-        const int at = min(4 * s + (int)((threadIdx.x & 63) >> 4), groups - 1);
+// Row of a 16-row tile whose result lane 16g + c holds after few_rows, and the row of its loads h = 0, 1
+__device__ __forceinline__ int few_row(int c) { return (c >> 1) + 8 * (c & 1); }
+
+struct FewSums {
+    f32x4_t v[2][2];  // [rows 0..7 or 8..15][half of X]
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            w[u][t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wc[t] + 16 * at));
-            sc[u][t] = ws[t][at];
-        }
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) v[h][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    __device__ __forceinline__ void start(int first, int by, int end) {
+    // X rows 4g .. 4g + 3 times row few_row(c) of the tile, in lane 16g + c
+    __device__ __forceinline__ f32x4_t rows() const {
+        const bool odd = threadIdx.x & 1;
+        f32x4_t r;
 #pragma unroll
-        for (int u = 0; u < DEPTH; ++u) {
-            load(u, min(first + u * by, end - 1));
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-    __device__ __forceinline__ void run(const uint8_t* x, int first, int by, int end, int s0, f32x4_t (&acc)[RT]) {
-        for (int s = first; s < end; s += DEPTH * by) {
+        for (int i = 0; i < 4; ++i) {
+            float s[2];
 #pragma unroll
-            for (int u = 0; u < DEPTH; ++u) {
-                const int at = s + u * by;
-                if (at >= end) break;
-                const uint8_t* p = x + 256 * (at - s0);
-                bf16x8_t a[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) a[j] = *reinterpret_cast<const bf16x8_t*>(p + 16 * j);
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const float f = mx4_scale(sc[u][t]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], mx4_to_bf16(w[u][t][j], f), acc[t], 0, 0, 0);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-                load(u, min(at + DEPTH * by, end - 1));
-                __builtin_amdgcn_sched_barrier(0);
+            for (int h = 0; h < 2; ++h) {
+                const float own = odd ? v[h][1][i] : v[h][0][i];
+                s[h] = own + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(own), 0xB1, 0xF, 0xF, false));
             }
+            r[i] = odd ? s[1] : s[0];
+        }
+        return r;
+    }
+};
+
+// The wavefront's steps s = first, first + by, ... < end over RT tiles of W, with X staged from step s0 on.
+template <int RT>
+struct FewStream {
+    u32x4_t w[RT][2];
+    uint32_t sc[RT][2];
+    const uint8_t *wc[RT][2], *ws[RT][2];
+    int groups;
+    // row(r): {codes, scales} of row r of tile t
+    template <typename Row>
+    __device__ __forceinline__ void tile(int t, Row row) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const Mx4Mat m = row(8 * h + (int)(threadIdx.x & 15) / 2);
+            wc[t][h] = m.codes;
+            ws[t][h] = m.scale;
+        }
+    }
+    __device__ __forceinline__ void load(int s) {  // past the end: the last group (against zeros of X)
+        const int lane = threadIdx.x & 63, at = min(8 * s + 4 * (lane & 1) + (lane >> 4), groups - 1);
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                w[t][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wc[t][h] + 16 * at));
+                sc[t][h] = ws[t][h][at];
+            }
+    }
+    // load(first) has been called. x: this lane's row of X in LDS, at byte 64 g
+    __device__ __forceinline__ void run(const uint8_t* x, int first, int by, int end, int s0, FewSums (&acc)[RT]) {
+        for (int s = first; s < end; s += by) {
+            const uint8_t* p = x + 2 * kFewK * (s - s0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bf16x8_t a0 = *reinterpret_cast<const bf16x8_t*>(p + 16 * j);
+                const bf16x8_t a1 = *reinterpret_cast<const bf16x8_t*>(p + kFewK + 16 * j);
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const bf16x8_t b = mx4_to_bf16(w[t][h][j], mx4_scale(sc[t][h]));
+                        acc[t].v[h][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[t].v[h][0], 0, 0, 0);
+                        acc[t].v[h][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[t].v[h][1], 0, 0, 0);
+                    }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            load(min(s + by, end - 1));
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 };

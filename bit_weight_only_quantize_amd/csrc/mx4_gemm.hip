@@ -32,7 +32,8 @@ static constexpr int64_t kGemvMaxK = 65536;  // x in LDS: 128 KiB
 
 static hipError_t launch_gemv1(const Mx4Mat& W, const uint16_t* x, void* Y, bool y_bf16, hipStream_t st) {
     const int lds = gemv_lds_bytes((int)W.K);
-    (void)hipFuncSetAttribute((const void*)mx4_gemv_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    static uint64_t asked;
+    if (const hipError_t e = allow_lds(mx4_gemv_kernel, lds, kMostLds, &asked)) return e;
     hipLaunchKernelGGL(mx4_gemv_kernel, dim3((unsigned)((W.N + kGemvWaves - 1) / kGemvWaves)), dim3(64 * kGemvWaves), lds, st,
                        W, x, Y, y_bf16);
     return hipGetLastError();
@@ -40,12 +41,10 @@ static hipError_t launch_gemv1(const Mx4Mat& W, const uint16_t* x, void* Y, bool
 
 // ---- up to 16 rows of bf16 (mx4_few.hpp): one workgroup of 16 wavefronts a CU owns consecutive
 // tiles of 16 rows of W, `side` of them at a time with 16 / side wavefronts on each one's steps
-// (their sums meet in LDS, in a fixed order), over X staged `chunk` steps at a time. One load of
-// codes in flight a wavefront: 18.5 us for 13 rows, 5120 -> 13824, against 20.7 with two and 21.5 with four; eight
-// wavefronts 20.8. Direct lane loads of X took 20 to 40.
+// (their sums meet in LDS, in a fixed order), over X staged `chunk` steps at a time. One step of codes in
+// flight a wavefront: 13.7 us for 13 rows, 5120 -> 13824 (14.8 with up to four tiles side by side; 15.5 and 15.9 with
+// two and three steps in flight). 80 us (5.1 TB/s) for 2 rows, 5120 -> 152064.
 constexpr int kFewWaves = 16;
-
-
 
 __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4Mat W, Mx4X X, int M, void* __restrict__ Y,
                                                                  int y_bf16, int64_t y_stride, int tiles, int side,
@@ -54,23 +53,25 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4Mat W, Mx4X 
     __shared__ f32x4_t sums[kFewWaves][64];
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int K = (int)W.K, steps = (K + 127) / 128, by = kFewWaves / side;
+    const int K = (int)W.K, steps = few_steps(K), by = kFewWaves / side;
     const int mine = wave / by, ks = wave % by;
     const int first = (int)((int64_t)tiles * blockIdx.x / gridDim.x);
     const int last = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
     const uint8_t* x = lds + min(c, M - 1) * few_row_bytes(chunk) + 64 * g;
-    FewStream<1, 1> f;
+    FewStream<1> f;
     f.groups = K / kMxGroup;
     bool staged = false;
     for (int t0 = first; t0 < last; t0 += side) {
         const bool live = mine < side && t0 + mine < last;
-        const int64_t n = min((int64_t)(t0 + mine) * 16 + c, W.N - 1);
-        f.wc[0] = W.codes + n * (K / 2);
-        f.ws[0] = W.scale + n * (K / 32);
-        f32x4_t acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+        f.tile(0, [&](int r) {
+            const int64_t n = min((int64_t)(t0 + mine) * 16 + r, W.N - 1);
+            return Mx4Mat{W.codes + n * (K / 2), W.scale + n * (K / 32), 0, 0};
+        });
+        FewSums acc[1];
+        acc[0].clear();
         for (int s0 = 0; s0 < steps; s0 += chunk) {
             const int end = min(s0 + chunk, steps);
-            if (live) f.start(min(s0 + ks, end - 1), by, end);
+            if (live) f.load(min(s0 + ks, end - 1));
             if (!staged || chunk < steps) {
                 __syncthreads();  // the chunk before has been read
                 few_stage(lds, [&](int r) { return X.x + r * X.row_stride; }, M, K, s0, chunk);
@@ -80,12 +81,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4Mat W, Mx4X 
             if (live) f.run(x, s0 + ks, by, end, s0, acc);
         }
         __syncthreads();  // the tiles before have been written
-        sums[wave][lane] = acc[0];
+        sums[wave][lane] = acc[0].rows();
         __syncthreads();
         if (wave < side && t0 + wave < last) {
             f32x4_t v = sums[wave * by][lane];
             for (int k = 1; k < by; ++k) v += sums[wave * by + k][lane];
-            const int64_t col = (int64_t)(t0 + wave) * 16 + c;
+            const int64_t col = (int64_t)(t0 + wave) * 16 + few_row(c);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 if (4 * g + r < M && col < W.N) {
@@ -99,18 +100,19 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4Mat W, Mx4X 
 
 static hipError_t launch_few(const Mx4Mat& W, const Mx4X& X, int64_t M, void* Y, bool y_bf16, int64_t y_stride,
                              hipStream_t st) {
-    const int tiles = (int)((W.N + 15) / 16), steps = (int)((W.K + 127) / 128);
+    const int tiles = (int)((W.N + 15) / 16), steps = few_steps(W.K);
     int chunk = steps;  // all of X in LDS, or as even pieces as there must be
-    const int room = 144 << 10;
+    const int room = kMostLds;
     if (few_row_bytes(steps) * M > room) {
-        const int most = (int)((room / M - 16) / 256);
+        const int most = (int)((room / M - 16) / (2 * kFewK));
         const int n = (steps + most - 1) / most;
         chunk = (steps + n - 1) / n;
     }
     const int grid = tiles < 256 ? tiles : 256, per = (tiles + grid - 1) / grid;
-    const int side = per < 4 ? per : 4, lds = few_row_bytes(chunk) * (int)M;
+    const int side = per < 8 ? per : 8, lds = few_row_bytes(chunk) * (int)M;
     auto kern = mx4_few_kernel;
-    (void)hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    static uint64_t asked;
+    if (const hipError_t e = allow_lds(kern, lds, kMostLds, &asked)) return e;
     hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * kFewWaves), lds, st, W, X, (int)M, Y, y_bf16, y_stride, tiles, side,
                        chunk);
     return hipGetLastError();
@@ -119,59 +121,69 @@ static hipError_t launch_few(const Mx4Mat& W, const Mx4X& X, int64_t M, void* Y,
 // ---- up to 16 rows of 4 bits: a workgroup of four wavefronts owns 32 rows of W, each every fourth step
 __global__ __launch_bounds__(256) void mx4_few_x4_kernel(Mx4Mat W, Mx4X X, int M, void* __restrict__ Y, int y_bf16,
                                                          int64_t y_stride) {
-    constexpr int RT = 2, KS = 4, U = 4;
+    constexpr int RT = 2, KS = 4, U = 2;
     __shared__ f32x4_t sums[KS][RT][64];
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
     const int m = min(c, M - 1), groups = (int)W.K / kMxGroup;
     const uint8_t *xc = X.codes + m * (W.K / 2), *xs = X.scale + m * (W.K / 32);
-    const uint8_t *wc[RT], *ws[RT];
-    f32x4_t acc[RT];
+    const uint8_t *wc[RT][2], *ws[RT][2];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        const int64_t n = min(n0 + 16 * t + c, W.N - 1);
-        wc[t] = W.codes + n * (W.K / 2);
-        ws[t] = W.scale + n * (W.K / 32);
-        acc[t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
-    for (int s = wave; 4 * s < groups; s += U * KS) {
-        u32x4_t w[U][RT], xv[U];  // all loads of U steps first
-        uint32_t sw[U][RT], sx[U];
-        bool in[U];
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = 4 * (s + u * KS) + g, at = min(k, groups - 1);
-            in[u] = k < groups;  // past the end: the last group again, against zeros of X
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                w[u][t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wc[t] + 16 * at));
-                sw[u][t] = ws[t][at];
-            }
-            xv[u] = *reinterpret_cast<const u32x4_t*>(xc + 16 * at);
-            sx[u] = xs[at];
+        for (int h = 0; h < 2; ++h) {
+            const int64_t n = min(n0 + 16 * t + 8 * h + c / 2, W.N - 1);
+            wc[t][h] = W.codes + n * (W.K / 2);
+            ws[t][h] = W.scale + n * (W.K / 32);
         }
+    FewSums acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t].clear();
+    for (int s = wave; 8 * s < groups; s += U * KS) {
+        u32x4_t w[U][RT][2], xv[U][2];  // all loads of U steps first
+        uint32_t sw[U][RT][2], sx[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!in[u]) {
-                xv[u] = u32x4_t{0, 0, 0, 0};
-                sx[u] = 0;
-            }
-            const auto wide = [](const u32x4_t& v) { return i32x8_t{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0}; };
+            const int k0 = 8 * (s + u * KS), at = min(k0 + 4 * (lane & 1) + g, groups - 1);
 #pragma unroll
             for (int t = 0; t < RT; ++t)
-                acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(xv[u]), wide(w[u][t]), acc[t], 4, 4, 0,
-                                                                          (int)sx[u], 0, (int)sw[u][t]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    w[u][t][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(wc[t][h] + 16 * at));
+                    sw[u][t][h] = ws[t][h][at];
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // past the end: the last group again, against zeros of X
+                const int k = k0 + 4 * i + g, ax = min(k, groups - 1);
+                xv[u][i] = *reinterpret_cast<const u32x4_t*>(xc + 16 * ax);
+                sx[u][i] = xs[ax];
+                if (k >= groups) {
+                    xv[u][i] = u32x4_t{0, 0, 0, 0};
+                    sx[u][i] = 0;
+                }
+            }
         }
+        const auto wide = [](const u32x4_t& v) { return i32x8_t{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0}; };
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        acc[t].v[h][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            wide(xv[u][i]), wide(w[u][t][h]), acc[t].v[h][i], 4, 4, 0, (int)sx[u][i], 0, (int)sw[u][t][h]);
     }
 #pragma unroll
-    for (int t = 0; t < RT; ++t) sums[wave][t][lane] = acc[t];
+    for (int t = 0; t < RT; ++t) sums[wave][t][lane] = acc[t].rows();
     __syncthreads();
     if (wave >= RT) return;
     f32x4_t v = sums[0][wave][lane];
 #pragma unroll
     for (int k = 1; k < KS; ++k) v += sums[k][wave][lane];
-    const int64_t n = n0 + 16 * wave + c;
+    const int64_t n = n0 + 16 * wave + few_row(c);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
         if (4 * g + r < M && n < W.N) {
@@ -288,7 +300,8 @@ static hipError_t launch_block(BlockArgs a, hipStream_t st) {
     a.tiles = (int)(tm * tn);
     const int lds = kStages * (X4 ? mx4_stage_bytes_x4<BM, BN>() : mx4_stage_bytes<BM, BN>());
     auto kern = mx4_block_kernel<X4, BM, BN, WM, WN>;
-    (void)hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    static uint64_t asked;
+    if (const hipError_t e = allow_lds(kern, lds, lds, &asked)) return e;
     hipLaunchKernelGGL(kern, dim3((unsigned)((a.tiles * a.parts + 7) / 8 * 8)), dim3(64 * WM * WN), lds, st, a);
     if (a.parts > 1)
         hipLaunchKernelGGL((mx4_block_sum_kernel<BM, BN, WM, WN>), dim3((unsigned)(a.tiles * (BM / WM / 32) * (BN / WN / 32))),

@@ -30,7 +30,7 @@ constexpr int64_t kDirectPairs = 16;
 static MoeWay moe_way(int64_t M, int k, int64_t E, int64_t D, int64_t F) {
     const int64_t P = M * k;
     if (P <= kDirectPairs && k * F <= (32 << 10) && D <= (64 << 10)) return {true, 0};
-    const int64_t each = P / E, room = (144 << 10) / (2 * (D > F ? D : F) + 272);  // rows that fit in LDS
+    const int64_t each = P / E, room = kMostLds / (2 * (D > F ? D : F) + 2 * kFewK + 16);  // rows that fit in LDS
     if (each <= 6 && room >= 8) return {false, 8};
     if (each <= 16 && room >= 16) return {false, 16};
     return {false, each <= 64 ? 64 : 128};
@@ -208,7 +208,8 @@ __device__ __forceinline__ int4 moe_tile(const int4* tiles, int nb, int& block) 
 }
 
 // ---------------------------------------------------------------- tiles of up to 16 rows
-// Wavefront w takes 16 gate rows and the same 16 up rows (or 16 down rows) and all of K.
+// Wavefront w takes 16 gate rows and the same 16 up rows (or 16 down rows) and all of K. 61 tokens over 128
+// experts of 768 x 2048, top 8: gate/up 73 us (209 MB; 2, 6 or 8 wavefronts 75 to 81), down 25 (105 MB).
 template <bool GU, int NW>
 __global__ __launch_bounds__(64 * NW) void mx4_moe_few_kernel(Mx4Moe a, const int4* __restrict__ tiles,
                                                               const int32_t* __restrict__ pairs, uint16_t* h,
@@ -221,32 +222,34 @@ __global__ __launch_bounds__(64 * NW) void mx4_moe_few_kernel(Mx4Moe a, const in
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t N = GU ? a.F : a.D, n0 = ((int64_t)block * NW + wave) * 16;
-    const int K = (int)(GU ? a.D : a.F), steps = (K + 127) / 128;
-    const int64_t row = (int64_t)t.x * N + min(n0 + c, N - 1);
-    FewStream<RT, GU ? 2 : 3> f;
+    const int K = (int)(GU ? a.D : a.F), steps = few_steps(K);
+    FewStream<RT> f;
     f.groups = K / kMxGroup;
-    f.wc[0] = (GU ? a.gate.codes : a.down.codes) + row * (K / 2);
-    f.ws[0] = (GU ? a.gate.scale : a.down.scale) + row * (K / 32);
-    if constexpr (GU) {
-        f.wc[1] = a.up.codes + row * (K / 2);
-        f.ws[1] = a.up.scale + row * (K / 32);
-    }
-    f32x4_t acc[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    f.start(0, 1, steps);
+    for (int i = 0; i < RT; ++i)
+        f.tile(i, [&](int r) {
+            const Mx4Mat& w = !GU ? a.down : i ? a.up : a.gate;
+            const int64_t row = (int64_t)t.x * N + min(n0 + r, N - 1);
+            return Mx4Mat{w.codes + row * (K / 2), w.scale + row * (K / 32), 0, 0};
+        });
+    FewSums acc[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[i].clear();
+    f.load(0);
     few_stage(lds, [&](int r) { return GU ? a.x + (pairs[t.y + r] / a.k) * a.x_stride : h + (int64_t)(t.y + r) * K; }, t.z, K,
               0, steps);
     __syncthreads();
     if (n0 >= N) return;
     f.run(lds + min(c, t.z - 1) * few_row_bytes(steps) + 64 * g, 0, 1, steps, 0, acc);
-    if (n0 + c >= N) return;
+    const int64_t n = n0 + few_row(c);
+    if (n >= N) return;
+    const f32x4_t v = acc[0].rows(), u = acc[RT - 1].rows();
 #pragma unroll
     for (int r = 0; r < 4; ++r)
         if (4 * g + r < t.z) {
-            const int64_t at = (int64_t)(t.y + 4 * g + r) * N + n0 + c;
-            if constexpr (GU) h[at] = to_bf16(gated(acc[0][r], acc[1][r], a.act));
-            else part[at] = to_bf16(acc[0][r]);
+            const int64_t at = (int64_t)(t.y + 4 * g + r) * N + n;
+            if constexpr (GU) h[at] = to_bf16(gated(v[r], u[r], a.act));
+            else part[at] = to_bf16(v[r]);
         }
 }
 
@@ -329,15 +332,18 @@ __global__ __launch_bounds__(256) void mx4_combine_kernel(Mx4Moe a, const int32_
 }
 
 template <int BM, int BN, int WM, int WN>
-static void launch_moe_blocks(const Mx4Moe& a, int64_t slots, const int4* tiles, const int32_t* pairs, uint16_t* h,
+static hipError_t launch_moe_blocks(const Mx4Moe& a, int64_t slots, const int4* tiles, const int32_t* pairs, uint16_t* h,
                               uint16_t* part, hipStream_t st) {
     const int lds = kStages * mx4_stage_bytes<BM, BN>(), nf = (int)((a.F + BN / 2 - 1) / (BN / 2)), nd = (int)((a.D + BN - 1) / BN);
     auto gu = mx4_moe_block_kernel<true, BM, BN, WM, WN>;
     auto down = mx4_moe_block_kernel<false, BM, BN, WM, WN>;
-    (void)hipFuncSetAttribute((const void*)gu, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    (void)hipFuncSetAttribute((const void*)down, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    static uint64_t asked_gu;
+    if (const hipError_t e = allow_lds(gu, lds, lds, &asked_gu)) return e;
+    static uint64_t asked_down;
+    if (const hipError_t e = allow_lds(down, lds, lds, &asked_down)) return e;
     hipLaunchKernelGGL(gu, dim3((unsigned)(slots * nf)), dim3(64 * WM * WN), lds, st, a, tiles, pairs, h, part, nf);
     hipLaunchKernelGGL(down, dim3((unsigned)(slots * nd)), dim3(64 * WM * WN), lds, st, a, tiles, pairs, h, part, nd);
+    return hipGetLastError();
 }
 
 hipError_t launch_mx4_moe(const Mx4Moe& a, void* work, hipStream_t st) {
@@ -354,7 +360,8 @@ hipError_t launch_mx4_moe(const Mx4Moe& a, void* work, hipStream_t st) {
         const dim3 gu((unsigned)((a.F + kDirectWaves - 1) / kDirectWaves), (unsigned)(a.M * a.k));
         const dim3 gd((unsigned)((a.D + kDirectWaves - 1) / kDirectWaves), (unsigned)a.M);
         const int lds = gemv_lds_bytes((int)a.D);
-        (void)hipFuncSetAttribute((const void*)mx4_gate_up_one_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    static uint64_t asked;
+    if (const hipError_t e = allow_lds(mx4_gate_up_one_kernel, lds, kMostLds, &asked)) return e;
         hipLaunchKernelGGL(mx4_gate_up_one_kernel, gu, dim3(64 * kDirectWaves), lds, st, a, h);
         hipLaunchKernelGGL(mx4_down_one_kernel, gd, dim3(64 * kDirectWaves), gemv_lds_bytes((int)(a.k * a.F)), st, a, h);
         return hipGetLastError();
@@ -364,17 +371,18 @@ hipError_t launch_mx4_moe(const Mx4Moe& a, void* work, hipStream_t st) {
     if (way.rows <= 16) {
         constexpr int GW = 4, DW = 8;
         const int nf = (int)((a.F + 16 * GW - 1) / (16 * GW)), nd = (int)((a.D + 16 * DW - 1) / (16 * DW));
-        const int lg = way.rows * few_row_bytes((int)(a.D + 127) / 128), ld = way.rows * few_row_bytes((int)(a.F + 127) / 128);
+        const int lg = way.rows * few_row_bytes(few_steps(a.D)), ld = way.rows * few_row_bytes(few_steps(a.F));
         auto gu = mx4_moe_few_kernel<true, GW>;
         auto down = mx4_moe_few_kernel<false, DW>;
-        (void)hipFuncSetAttribute((const void*)gu, hipFuncAttributeMaxDynamicSharedMemorySize, lg);
-        (void)hipFuncSetAttribute((const void*)down, hipFuncAttributeMaxDynamicSharedMemorySize, ld);
+        static uint64_t asked_gu, asked_down;
+        if (const hipError_t e = allow_lds(gu, lg, kMostLds, &asked_gu)) return e;
+        if (const hipError_t e = allow_lds(down, ld, kMostLds, &asked_down)) return e;
         hipLaunchKernelGGL(gu, dim3((unsigned)(L.slots * nf)), dim3(64 * GW), lg, st, a, tiles, pairs, h, part, nf);
         hipLaunchKernelGGL(down, dim3((unsigned)(L.slots * nd)), dim3(64 * DW), ld, st, a, tiles, pairs, h, part, nd);
-    } else if (way.rows == 64) {
-        launch_moe_blocks<64, 256, 1, 4>(a, L.slots, tiles, pairs, h, part, st);
     } else {
-        launch_moe_blocks<128, 128, 2, 2>(a, L.slots, tiles, pairs, h, part, st);
+        const hipError_t e = way.rows == 64 ? launch_moe_blocks<64, 256, 1, 4>(a, L.slots, tiles, pairs, h, part, st)
+                                            : launch_moe_blocks<128, 128, 2, 2>(a, L.slots, tiles, pairs, h, part, st);
+        if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL(mx4_combine_kernel, dim3((unsigned)a.M), dim3(256), 0, st, a, place, part);
     return hipGetLastError();

@@ -41,16 +41,23 @@ __device__ __forceinline__ double wave_sum_d(double v) {
     return v;
 }
 
+// LDS written by this wavefront's lanes, before others of them read it
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 template <bool BF16>
 __device__ __forceinline__ float logit(const SelectArgs& a, int64_t m, int e) {
     const int64_t at = m * a.row_stride + e;
     return BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
 }
 
-// A token with everything in 64 bits; lane holds the experts lane + 64 j. values: [1024] in LDS.
+// A token with everything in 64 bits; lane holds the experts lane + 64 j. values: [64 EPL] in LDS.
 template <int EPL, bool BF16>
 __device__ void select_exact(const SelectArgs& a, int64_t m, double* values) {
-    const int lane = threadIdx.x;
+    const int lane = threadIdx.x & 63;
     float l[EPL];
     float mx = -INFINITY;
 #pragma unroll
@@ -89,7 +96,7 @@ __device__ void select_exact(const SelectArgs& a, int64_t m, double* values) {
             const int e = lane + 64 * j;
             if (e < a.E) values[e] = !(l[j] > -INFINITY) ? -INFINITY : p[j] + (a.bias ? (double)a.bias[e] : 0.0);
         }
-        __syncthreads();
+        wave_lds_sync();
         double v = 0;
         if (lane < a.groups) {
             double b0 = -INFINITY, b1 = -INFINITY;
@@ -153,11 +160,15 @@ __device__ void select_exact(const SelectArgs& a, int64_t m, double* values) {
 // relative error, and units for the sum and the reciprocal: within 2^-21. c's rounding: 2^-24 |c|.
 constexpr float kSoftmaxOff = 0x1p-19f, kSigmoidOff = 0x1p-21f;
 
+constexpr int kSelectWaves = 4;
+
 template <int EPL, bool BF16>
-__global__ __launch_bounds__(64) void moe_select_kernel(SelectArgs a) {
-    __shared__ double values[1024];
-    const int lane = threadIdx.x;
-    const int64_t m = blockIdx.x;
+__global__ __launch_bounds__(64 * kSelectWaves) void moe_select_kernel(SelectArgs a) {
+    __shared__ double all[kSelectWaves][64 * EPL];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    double* values = all[wave];
+    const int64_t m = (int64_t)blockIdx.x * kSelectWaves + wave;
+    if (m >= a.M) return;  // wavefronts share nothing
     float l[EPL], c[EPL];
     float mx = -INFINITY;
     bool nan = false;
@@ -211,7 +222,7 @@ __global__ __launch_bounds__(64) void moe_select_kernel(SelectArgs a) {
             const int e = lane * EPL + j;
             if (e < a.E) vals[e] = c[j];
         }
-        __syncthreads();
+        wave_lds_sync();
         int share = 1;
         while (2 * share * a.groups <= 64) share *= 2;
         const int g = lane / share;
@@ -307,7 +318,7 @@ __global__ __launch_bounds__(64) void moe_select_kernel(SelectArgs a) {
 }
 
 hipError_t launch_moe_select(const SelectArgs& a, bool bf16, hipStream_t st) {
-    const dim3 grid((unsigned)a.M), block(64);
+    const dim3 grid((unsigned)((a.M + kSelectWaves - 1) / kSelectWaves)), block(64 * kSelectWaves);
 #define W4_SELECT(EPL)                                                                                   \
     if (a.E <= 64 * EPL) {                                                                               \
         if (bf16) hipLaunchKernelGGL((moe_select_kernel<EPL, true>), grid, block, 0, st, a);             \
