@@ -89,8 +89,9 @@ struct SelectArgs {
     int64_t M;
     int E, k, sigmoid, groups, top_groups, best, renormalize;
     float scale;
+    int size, share;  // of the launcher: experts a group, log2 of lanes a group
 };
-hipError_t launch_moe_select(const SelectArgs& a, bool bf16, hipStream_t st);
+hipError_t launch_moe_select(SelectArgs a, bool bf16, hipStream_t st);
 
 // ---- experts' products (mx4_moe.hip)
 struct Mx4Moe {

@@ -8,8 +8,9 @@
 //     decision (each chosen expert against the next, kept groups against the best other one) has to
 //     have a margin beyond it. A token without (ties, mostly) is done again in 64 bits.
 // Sorting is k rounds of a wave-wide maximum over 32-bit keys; a lane holds consecutive experts, so the
-// first lane with the maximum has the lowest index. Bound by instruction issue: 8192 tokens, 256 experts in
-// 8 groups, top 8, sigmoid with bias: 21 us (27 with everything in 64 bits; 1.7 for the bytes). Finding the k-th key bit by
+// first lane with the maximum has the lowest index. Bound by its dependent steps and instruction issue (920 vector
+// instructions a token): 8192 tokens, 256 experts in
+// 8 groups, top 8, sigmoid with bias: 20 us (27 with everything in 64 bits; 1.7 for the bytes). Finding the k-th key bit by
 // bit with ballots instead of the rounds, and ranking what it leaves, took 26.
 #include "mx4.hpp"
 #include "topk.hpp"
@@ -91,7 +92,7 @@ __device__ void select_exact(const SelectArgs& a, int64_t m, double* values) {
         key[j] = e >= a.E ? 0 : masked || c != c ? 1 : order_key(c);
     }
     if (a.groups > 1) {
-        const int size = a.E / a.groups;
+        const int size = a.size;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const int e = lane + 64 * j;
@@ -214,7 +215,8 @@ __global__ __launch_bounds__(64 * kSelectWaves) void moe_select_kernel(SelectArg
     }
     bool close = false;  // some decision is within the errors; an infinite or NaN c compares so too
     uint64_t kept = ~0ull;
-    const int size = a.E / a.groups;
+    const int size = a.size;
+    const float per = 1.f / (float)size;  // (e + .5) per: its integer part is e / size, as e < 1024
     if (grouped) {
         // `share` lanes (a power of two) scan a group, then merge their two largest
         float* vals = reinterpret_cast<float*>(values);
@@ -224,9 +226,8 @@ __global__ __launch_bounds__(64 * kSelectWaves) void moe_select_kernel(SelectArg
             if (e < a.E) vals[e] = c[j];
         }
         wave_lds_sync();
-        int share = 1;
-        while (2 * share * a.groups <= 64) share *= 2;
-        const int g = lane / share;
+        const int share = 1 << a.share;
+        const int g = lane >> a.share;
         float b0 = -INFINITY, b1 = -INFINITY, big = 0.f;
         if (g < a.groups)
             for (int i = lane & (share - 1); i < size; i += share) {
@@ -253,7 +254,7 @@ __global__ __launch_bounds__(64 * kSelectWaves) void moe_select_kernel(SelectArg
         for (int r = 0; r < a.top_groups; ++r) {
             last = wave_max_u(gk);
             const int at = __ffsll((unsigned long long)__ballot(gk == last)) - 1;
-            kept |= 1ull << (at / share);
+            kept |= 1ull << (at >> a.share);
             if (lane == at) gk = 0;
         }
         const uint32_t next = wave_max_u(gk);
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(64 * kSelectWaves) void moe_select_kernel(SelectArg
     for (int j = 0; j < EPL; ++j) {
         const int e = lane * EPL + j;
         const float v = by_logit ? l[j] : c[j];
-        const bool can = e < a.E && (!grouped || ((kept >> (e / size)) & 1));
+        const bool can = e < a.E && (!grouped || ((kept >> (int)(((float)e + 0.5f) * per)) & 1));
         if (!by_logit) close |= v != v;
         key[j] = !can ? 0u : l[j] > -INFINITY ? order_key(v) : 1u;
     }
@@ -318,7 +319,10 @@ __global__ __launch_bounds__(64 * kSelectWaves) void moe_select_kernel(SelectArg
     }
 }
 
-hipError_t launch_moe_select(const SelectArgs& a, bool bf16, hipStream_t st) {
+hipError_t launch_moe_select(SelectArgs a, bool bf16, hipStream_t st) {
+    a.size = a.E / a.groups;
+    a.share = 0;
+    while (2 * (a.groups << a.share) <= 64) ++a.share;
     const dim3 grid((unsigned)((a.M + kSelectWaves - 1) / kSelectWaves)), block(64 * kSelectWaves);
 #define W4_SELECT(EPL)                                                                                   \
     if (a.E <= 64 * EPL) {                                                                               \
