@@ -986,14 +986,17 @@ int w4_kv_attention(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4
 }
 
 // ---------------------------------------------------------------- microscaled 4-bit
+// Rows (a launch holds under 2^32 threads, up to 64 a row) and columns (bytes of 16 rows in 31 bits)
+static const int64_t kMxRows = 1 << 26, kMxColumns = 1 << 24;
+
 // One matrix, or a stack of any number of them (experts == 0)
 static int mx4_check(const w4_matrix* W, const char* name, int experts) {
     if (!W) return fail(W4_EINVAL, "%s: null descriptor", name);
     if (W->scheme != W4_MX4_G32) return fail(W4_EINVAL, "%s: scheme %d, not W4_MX4_G32", name, (int)W->scheme);
     if (W->num_experts < 1 || (experts && W->num_experts != experts))
         return fail(W4_ESHAPE, "%s: num_experts %d", name, (int)W->num_experts);
-    if (W->N < 0 || W->K <= 0 || W->N > kInt31 || W->K > kInt31 || W->K % w4::kMxGroup)
-        return fail(W4_ESHAPE, "%s: N=%lld K=%lld (K must be a multiple of %d, both under 2^31)", name,
+    if (W->N < 0 || W->K <= 0 || W->N > kMxRows || W->K > kMxColumns || W->K % w4::kMxGroup)
+        return fail(W4_ESHAPE, "%s: N=%lld K=%lld (N up to 2^26, K up to 2^24 and a multiple of %d)", name,
                     (long long)W->N, (long long)W->K, w4::kMxGroup);
     if (W->N == 0) return W4_OK;
     if (!W->codes || !W->scale) return fail(W4_EINVAL, "%s: null codes or scale", name);
@@ -1024,8 +1027,8 @@ static int mx4_check_rows(const w4_rows* t, const char* name, int64_t rows, int6
 }
 
 int w4_mx4_quantize(const w4_rows* x, int64_t rows, int64_t K, void* codes, void* scale, void* stream) {
-    if (rows < 0 || rows > kInt31 || K <= 0 || K > kInt31 || K % w4::kMxGroup)
-        return fail(W4_ESHAPE, "rows=%lld K=%lld (K must be a positive multiple of %d, both under 2^31)",
+    if (rows < 0 || rows > kMxRows || K <= 0 || K > kMxColumns || K % w4::kMxGroup)
+        return fail(W4_ESHAPE, "rows=%lld K=%lld (rows up to 2^26, K up to 2^24 and a positive multiple of %d)",
                     (long long)rows, (long long)K, w4::kMxGroup);
     if (rows == 0) return ok();
     if (!codes || !scale) return fail(W4_EINVAL, "null codes or scale");
@@ -1048,8 +1051,8 @@ int w4_mx4_read(const w4_matrix* q, const w4_rows* out, void* stream) {
 }
 
 size_t w4_mx4_gemm_workspace_bytes(const w4_matrix* W, int64_t M, int x4) {
-    if (!W || W->scheme != W4_MX4_G32 || W->num_experts != 1 || W->N <= 0 || W->N > kInt31 || W->K <= 0 ||
-        W->K > kInt31 || W->K % w4::kMxGroup || M <= 0 || M > kInt31)
+    if (!W || W->scheme != W4_MX4_G32 || W->num_experts != 1 || W->N <= 0 || W->N > kMxRows || W->K <= 0 ||
+        W->K > kMxColumns || W->K % w4::kMxGroup || M <= 0 || M > kMxRows)
         return 0;
     return w4::mx4_gemm_workspace(M, W->N, W->K, x4 != 0);
 }
@@ -1072,7 +1075,7 @@ int w4_mx4_gemm(const w4_matrix* W, const w4_rows* X, int64_t M, const w4_rows* 
                 size_t workspace_bytes, void* stream) {
     int rc = mx4_check(W, "W", 1);
     if (rc) return rc;
-    if (M < 0 || M > kInt31) return fail(W4_ESHAPE, "M=%lld out of range", (long long)M);
+    if (M < 0 || M > kMxRows) return fail(W4_ESHAPE, "M=%lld out of range", (long long)M);
     if (M == 0 || W->N == 0) return ok();
     if ((rc = mx4_check_rows(X, "X", M, W->K, true, true))) return rc;
     return mx4_gemm_call(W, {(const uint16_t*)X->data, M > 1 ? X->row_stride : W->K, nullptr, nullptr}, M, Y,
@@ -1094,7 +1097,7 @@ int w4_moe_select(const w4_rows* logits, int64_t M, int64_t E, const w4_select* 
     if (!how) return fail(W4_EINVAL, "null selection");
     if (how->score != W4_SCORE_SOFTMAX && how->score != W4_SCORE_SIGMOID)
         return fail(W4_EINVAL, "unknown score %d", (int)how->score);
-    if (M < 0 || M > kInt31 || E < 1 || E > 1024)
+    if (M < 0 || M > kMxRows || E < 1 || E > 1024)
         return fail(W4_ESHAPE, "M=%lld E=%lld out of range", (long long)M, (long long)E);
     const int G = how->groups;
     if (G < 1 || G > 64 || E % G || how->top_groups < 1 || how->top_groups > G)
@@ -1132,7 +1135,7 @@ static const int64_t kMoePairs = 1 << 24;
 
 size_t w4_mx4_moe_workspace_bytes(int64_t M, int top_k, int64_t E, int64_t D, int64_t F) {
     if (M <= 0 || top_k < 1 || top_k > 32 || M > kMoePairs / top_k || E < 1 || E > 1024 || D < 1 || F < 1 ||
-        D > kInt31 || F > kInt31)
+        D > kMxColumns || F > kMxColumns)
         return 0;
     return w4::mx4_moe_workspace(M, top_k, E, D, F);
 }
@@ -1148,6 +1151,7 @@ int w4_mx4_moe(const w4_matrix* gate, const w4_matrix* up, const w4_matrix* down
     if (up->N != F || up->K != D || down->N != D || down->K != F)
         return fail(W4_ESHAPE, "expected gate/up [E][F][D] and down [E][D][F]");
     if (E > 1024) return fail(W4_ESHAPE, "E=%lld exceeds 1024", (long long)E);
+    if (D > kMxColumns || F > kMxColumns) return fail(W4_ESHAPE, "D=%lld and F=%lld: up to 2^24", (long long)D, (long long)F);
     if (act != W4_ACT_GELU_TANH && act != W4_ACT_SILU) return fail(W4_EINVAL, "unknown activation %d", act);
     if (top_k < 1 || top_k > 32) return fail(W4_ESHAPE, "top_k=%d out of range [1, 32]", top_k);
     if (M < 0 || M > kMoePairs / top_k)

@@ -295,7 +295,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_block_sum_kernel(BlockArgs a
 template <bool X4, int BM, int BN, int WM, int WN>
 static hipError_t launch_block(BlockArgs a, hipStream_t st) {
     const int64_t tm = (a.M + BM - 1) / BM, tn = (a.W.N + BN - 1) / BN;
-    if (tm * tn * a.parts > 0x7fffffff - 8) return hipErrorInvalidValue;
+    if (tm * tn * a.parts > 0xffffffffLL / (64 * WM * WN) - 8) return hipErrorInvalidValue;  // threads of a launch
     a.tiles_n = (int)tn;
     a.tiles = (int)(tm * tn);
     const int lds = kStages * (X4 ? mx4_stage_bytes_x4<BM, BN>() : mx4_stage_bytes<BM, BN>());

@@ -349,7 +349,7 @@ static hipError_t launch_moe_block(const Mx4Moe& a, int64_t slots, const int4* t
 hipError_t launch_mx4_moe(const Mx4Moe& a, void* work, hipStream_t st) {
     const Mx4MoeWork L = moe_layout(a.M, a.k, a.E, a.D, a.F);
     const MoeWay way = moe_way(a.M, a.k, a.E, a.D, a.F);
-    if (L.slots * ((a.D > a.F ? a.D : a.F) / 64 + 1) > 0x7fffffff) return hipErrorInvalidValue;
+    if (L.slots * ((a.D > a.F ? a.D : a.F) / 64 + 1) > 0xffffffffLL / 512) return hipErrorInvalidValue;  // threads of a launch
     uint8_t* base = (uint8_t*)work;
     int4* tiles = (int4*)(base + L.tiles);
     int32_t* pairs = (int32_t*)(base + L.pairs);

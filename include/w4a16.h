@@ -598,7 +598,8 @@ int w4_kv_attention(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4
  * that are written, only data has to be 16-byte aligned where nothing else is said.
  */
 
-/* x [rows][K], fp32 or bf16, to codes and scale of one matrix of `rows` rows. 0 <= rows < 2^31. */
+/* x [rows][K], fp32 or bf16, to codes and scale of one matrix of `rows` rows. Here and below a matrix
+ * has up to 2^26 rows and 2^24 columns. */
 int w4_mx4_quantize(const w4_rows* x, int64_t rows, int64_t K, void* codes, void* scale, void* stream);
 
 /* The values of q (one matrix) to out [N][K], fp32 or bf16 (exact in both, but for
@@ -611,11 +612,13 @@ int w4_mx4_read(const w4_matrix* q, const w4_rows* out, void* stream);
  * (w4a4_mx4_gemm: both sides in 4 bits go to the matrix cores as they are stored).
  * Y: fp32 or bf16 (nearest even), Y's row_stride >= N. Products are exact and sums
  * fp32; a row of X with an infinity or NaN gives what the sum gives, a NaN scale
- * NaN. W: one matrix. M, N < 2^31 and any size down to 0; K < 2^31. Any number of
+ * NaN. With bf16 X, numbers under 2^-126 (of X, or a code times its scale) may count
+ * as 0. W: one matrix; M (up to 2^26) and N may be 0. Any number of
  * rows takes the same call: few rows stream the weights, many fill matrix tiles.
  * workspace: w4_mx4_gemm_workspace_bytes(...) bytes (x4: whether X is quantized), 0 for
  * most sizes; contents on entry do not matter. Without it (NULL and 0 bytes) the
- * product takes fewer workgroups and longer. Y must not overlap the inputs. Deterministic;
+ * product takes fewer workgroups and longer. Calls sharing a workspace must not
+ * overlap. Y must not overlap the inputs. Deterministic;
  * the order of sums depends on the sizes, and on whether there is a workspace.
  */
 size_t w4_mx4_gemm_workspace_bytes(const w4_matrix* W, int64_t M, int x4);
@@ -640,7 +643,7 @@ int w4a4_mx4_gemm(const w4_matrix* W, const w4_matrix* X, const w4_rows* Y, void
  * gets weights 0. A NaN logit counts as masked and makes the token's weights NaN.
  * bias fp32 [E] or NULL; 1 <= top_k <= min(32, top_groups * E / groups); E <= 1024;
  * groups divides E, 1 <= top_groups <= groups <= 64, group_best <= E / groups.
- * ids int32 [M][top_k], weights fp32 [M][top_k]. 0 <= M < 2^31. Feeds w4a16_moe_gemv and
+ * ids int32 [M][top_k], weights fp32 [M][top_k]. 0 <= M <= 2^26. Feeds w4a16_moe_gemv and
  * w4_mx4_moe.
  */
 #define W4_SCORE_SOFTMAX 0
@@ -663,8 +666,8 @@ int w4_moe_select(const w4_rows* logits, int64_t M, int64_t E, const w4_select* 
  * [E][F][D]; down [E][D][F]; D and F multiples of 32. x bf16 [M][D]; y bf16 [M][D] with a
  * row stride >= D, not overlapping x. ids, weights [M][top_k] as w4_moe_select or w4_moe_route give them;
  * a slot whose id lies outside [0, E) contributes nothing, and a token without any gets
- * y = 0. An expert's weights are read once for all its tokens (once for 256 of them
- * or so). Sums are fp32, h and each expert's part of y are
+ * y = 0. An expert's weights are read once for a tile of its tokens (8 to 128,
+ * by how many an expert gets). Sums are fp32, h and each expert's part of y are
  * rounded to bf16. 0 <= M, M * top_k <= 2^24, top_k <= 32,
  * E <= 1024. workspace: w4_mx4_moe_workspace_bytes(...) bytes; its contents on entry do not
  * matter. Calls sharing a workspace must not overlap. Deterministic.

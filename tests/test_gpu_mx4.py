@@ -415,3 +415,98 @@ def test_binding_refuses():
         w4.mx4_moe(*q, x, ids, w, act="relu")
     with pytest.raises(w4.W4Error):
         w4.mx4_moe(*q, x, ids, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+# ---------------------------------------------------------------- far ends, calls side by side
+@pytest.mark.parametrize("x4", [False, True])
+@pytest.mark.parametrize("M", [1, 5, 40, 300])
+def test_weights_past_4_gib(M, x4):
+    """Only the last rows of a matrix of more than 2^32 code bytes are not zero."""
+    K, N = 65536, (1 << 17) + 19
+    W = w4.QuantizedMatrix("mx4_g32", N, K, torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda"),
+                           torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda"), None)
+    c, s, v = integers((3, K), 5)
+    W.codes[N - 3:] = torch.from_numpy(c).cuda()
+    W.scale[N - 3:] = torch.from_numpy(s).cuda()
+    xc, xs, xv = integers((M, K), M, 127, 128)
+    xc[:, 64:], xv[:, 128:] = 0, 0                       # few enough products that fp32 holds every partial sum
+    y = w4.mx4_gemm(W, device(xc, xs) if x4 else bf16(xv).cuda(), dtype=torch.float32)
+    want, _ = product(xv, v)
+    assert torch.equal(y[:, N - 3:].cpu().double(), want)
+    assert not bool(y[:, :N - 3].any())
+
+
+@pytest.mark.parametrize("M", [1, 20, 700])
+def test_stacks_past_4_gib(M):
+    E, F, D = 70, 2048, 65536
+    q = [w4.empty_quantized("mx4_g32", *s, num_experts=E) for s in ((F, D), (F, D), (D, F))]
+    for m in q:
+        m.codes.zero_()
+        m.scale.fill_(127)
+    gc, gs, gv = integers((2, D), 1, 120, 121)
+    for m in q[:2]:                                      # the last expert's last two rows of h
+        m.codes[E - 1, F - 2:] = torch.from_numpy(gc).cuda()
+        m.scale[E - 1, F - 2:] = torch.from_numpy(gs).cuda()
+    q[2].codes[E - 1, D - 1, F // 2 - 1] = 0x22          # 1 times the last two h
+    x = torch.zeros((M, D), dtype=torch.bfloat16)
+    x[:, :96] = torch.randn((M, 96), generator=torch.Generator().manual_seed(M)).to(torch.bfloat16)
+    ids = torch.full((M, 2), E - 1, dtype=torch.int32)
+    w = torch.full((M, 2), 0.5)
+    y = w4.mx4_moe(*q, x.cuda(), ids.cuda(), w.cuda()).cpu().double()
+    g = x[:, :96].double().numpy() @ gv[:, :96].T
+    want = oracle.gated(g, g, "gelu_tanh").sum(1)
+    size = np.abs(oracle.gated(g, g, "gelu_tanh")).sum(1)
+    # h to bf16, parts to bf16, y to bf16, and the activation's 2^-18
+    assert (np.abs(y[:, D - 1].numpy() - want) <= 2.0 ** -6 * size + 1e-6).all()
+    assert not bool(y[:, :D - 1].any())
+
+
+def test_calls_side_by_side_on_two_streams():
+    """Each with workspaces of its own, over the same weights."""
+    runs = [all_calls(M) for M in (40, 300)]
+    want = [run() for _, run in runs]
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(runs[i][1]())
+    torch.cuda.synchronize()
+    for i in range(2):
+        for outs in got[i]:
+            for a, b in zip(want[i], outs):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M", [1, 3, 40])
+def test_experts_without_a_usual_shape(M):
+    """More columns than LDS holds rows of, more experts than pairs, a token whose experts are all the same, weights of 0
+    and large ones, and an output row stride that is no multiple of 16 bytes."""
+    E, D, F, k = 40, 20480, 32, 2
+    q, v = stacks(E, D, F, 5)
+    g = torch.Generator().manual_seed(M)
+    x = torch.randn((M, D), generator=g).to(torch.bfloat16)
+    ids = torch.randint(0, E, (M, k), generator=g, dtype=torch.int32)
+    ids[0] = 7
+    w = torch.randn((M, k), generator=g) * 100
+    w[0, 1] = 0
+    y = torch.full((M, D + 3), -5.0, dtype=torch.bfloat16, device="cuda")
+    w4.mx4_moe(*q, x.cuda(), ids.cuda(), w.cuda(), "silu", out=y[:, :D])
+    want, bound = oracle.mx4_moe(*v, x.double().numpy(), ids.numpy(), w.double().numpy(), "silu")
+    got = y.cpu().double().numpy()
+    assert (np.abs(got[:, :D] - want) <= bound).all() and (got[:, D:] == -5).all()
+
+
+def test_pair_counts_at_the_borders_between_ways():
+    """One expert gets all pairs, or none, around every number of rows at which another kernel takes over."""
+    E, D, F = 2, 64, 32
+    q, v = stacks(E, D, F, 9)
+    for M in (15, 16, 17, 23, 24, 33, 34, 35, 63, 65, 127, 129, 641, 643):
+        x = torch.randn((M, D), generator=torch.Generator().manual_seed(M)).to(torch.bfloat16)
+        for e in (0, 1):
+            ids = torch.full((M, 1), e, dtype=torch.int32)
+            w = torch.ones((M, 1))
+            y = w4.mx4_moe(*q, x.cuda(), ids.cuda(), w.cuda()).cpu().double().numpy()
+            want, bound = oracle.mx4_moe(*v, x.double().numpy(), ids.numpy(), w.double().numpy(), "gelu_tanh")
+            assert (np.abs(y - want) <= bound).all(), (M, e)
