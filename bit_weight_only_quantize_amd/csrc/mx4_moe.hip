@@ -6,8 +6,8 @@
 //     y in one pass over its experts' down rows. Two launches, no sorting.
 //   * otherwise the pairs are sorted by expert (mx4_sort_kernel) into tiles of rows of one expert, so
 //     that an expert's weights are read once for a tile; the gate/up product writes h in sorted order,
-//     the down product each pair's part of y (rounded to bf16, as h is), and the last launch
-//     adds up a token's k parts in fp32 and in their order. Tiles of 8 or 16 rows stream
+//     the down product each pair's part of y in fp32 (parts in bf16 took 16-bit results from 2.4e-3 off to
+//     2.9e-3), and the last launch adds up a token's k parts in their order. Tiles of 8 or 16 rows stream
 //     the weights (mx4_few.hpp), tiles of 64 or 128 are blocks on the matrix cores (mx4_block.hpp).
 // A pair's place among its expert's is not fixed (it comes from an integer atomic), but its
 // results do not depend on it.
@@ -50,7 +50,7 @@ static Mx4MoeWork moe_layout(int64_t M, int k, int64_t E, int64_t D, int64_t F) 
     L.place = L.pairs + (way.direct ? 0 : up((size_t)P * 4));
     L.h = L.place + (way.direct ? 0 : up((size_t)P * 4));
     L.part = L.h + up((size_t)P * F * 2);
-    L.total = L.part + (size_t)P * D * 2;
+    L.total = L.part + (size_t)P * D * 4;
     return L;
 }
 size_t mx4_moe_workspace(int64_t M, int k, int64_t E, int64_t D, int64_t F) {
@@ -216,7 +216,7 @@ __device__ __forceinline__ int4 moe_tile(const int4* tiles, int nb, int& block) 
 template <bool GU, int NW>
 __global__ __launch_bounds__(64 * NW) void mx4_moe_few_kernel(Mx4Moe a, const int4* __restrict__ tiles,
                                                               const int32_t* __restrict__ pairs, uint16_t* h,
-                                                              uint16_t* __restrict__ part, int nb) {
+                                                              float* __restrict__ part, int nb) {
     extern __shared__ __align__(16) uint8_t lds[];
     constexpr int RT = GU ? 2 : 1;
     int block;
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(64 * NW) void mx4_moe_few_kernel(Mx4Moe a, const in
         if (4 * g + r < t.z) {
             const int64_t at = (int64_t)(t.y + 4 * g + r) * N + n;
             if constexpr (GU) h[at] = to_bf16(gated(v[r], u[r], a.act));
-            else part[at] = to_bf16(v[r]);
+            else part[at] = v[r];
         }
 }
 
@@ -261,7 +261,7 @@ __global__ __launch_bounds__(64 * NW) void mx4_moe_few_kernel(Mx4Moe a, const in
 template <bool GU, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_moe_block_kernel(Mx4Moe a, const int4* __restrict__ tiles,
                                                                         const int32_t* __restrict__ pairs, uint16_t* h,
-                                                                        uint16_t* __restrict__ part, int nb) {
+                                                                        float* __restrict__ part, int nb) {
     extern __shared__ __align__(16) uint8_t lds[];
     constexpr int NI = BM / WM / 32, NJ = BN / WN / 32, COLS = GU ? BN / 2 : BN;
     static_assert(NJ == 2, "a gate and an up tile");
@@ -298,15 +298,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_moe_block_kernel(Mx4Moe a
             if constexpr (GU) {
                 if (n < N) h[at] = to_bf16(gated(acc[i][0][r], acc[i][1][r], a.act));
             } else {
-                if (n < N) part[at] = to_bf16(acc[i][0][r]);
-                if (n + 32 < N) part[at + 32] = to_bf16(acc[i][1][r]);
+                if (n < N) part[at] = acc[i][0][r];
+                if (n + 32 < N) part[at + 32] = acc[i][1][r];
             }
         }
 }
 
 // ---------------------------------------------------------------- a token's parts
 __global__ __launch_bounds__(256) void mx4_combine_kernel(Mx4Moe a, const int32_t* __restrict__ place,
-                                                          const uint16_t* __restrict__ part) {
+                                                          const float* __restrict__ part) {
     const int64_t m = blockIdx.x;
     for (int64_t d = 8 * threadIdx.x; d < a.D; d += 8 * 256) {
         float y[8] = {};
@@ -314,11 +314,12 @@ __global__ __launch_bounds__(256) void mx4_combine_kernel(Mx4Moe a, const int32_
             const int p = place[m * a.k + j];
             if (p < 0) continue;
             const float w = a.weights[m * a.k + j];
-            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(part + (int64_t)p * a.D + d);
+            const f32x4_t* v = reinterpret_cast<const f32x4_t*>(part + (int64_t)p * a.D + d);
+            const f32x4_t lo = v[0], hi = v[1];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                y[2 * i] = fmaf(w, __uint_as_float(v[i] << 16), y[2 * i]);
-                y[2 * i + 1] = fmaf(w, __uint_as_float(v[i] & 0xFFFF0000u), y[2 * i + 1]);
+                y[i] = fmaf(w, lo[i], y[i]);
+                y[4 + i] = fmaf(w, hi[i], y[4 + i]);
             }
         }
         uint16_t* out = a.y + m * a.y_stride + d;
@@ -336,7 +337,7 @@ __global__ __launch_bounds__(256) void mx4_combine_kernel(Mx4Moe a, const int32_
 
 template <bool GU, int BM, int BN, int WM, int WN>
 static hipError_t launch_moe_block(const Mx4Moe& a, int64_t slots, const int4* tiles, const int32_t* pairs, uint16_t* h,
-                                   uint16_t* part, hipStream_t st) {
+                                   float* part, hipStream_t st) {
     const int64_t N = GU ? a.F : a.D;
     const int lds = kStages * mx4_stage_bytes<BM, BN>(), cols = GU ? BN / 2 : BN, nb = (int)((N + cols - 1) / cols);
     auto kern = mx4_moe_block_kernel<GU, BM, BN, WM, WN>;
@@ -355,7 +356,7 @@ hipError_t launch_mx4_moe(const Mx4Moe& a, void* work, hipStream_t st) {
     int32_t* pairs = (int32_t*)(base + L.pairs);
     int32_t* place = (int32_t*)(base + L.place);
     uint16_t* h = (uint16_t*)(base + L.h);
-    uint16_t* part = (uint16_t*)(base + L.part);
+    float* part = (float*)(base + L.part);
     if (way.direct) {
         const dim3 gu((unsigned)((a.F + kDirectWaves - 1) / kDirectWaves), (unsigned)(a.M * a.k));
         const dim3 gd((unsigned)((a.D + kDirectWaves - 1) / kDirectWaves), (unsigned)a.M);

@@ -667,8 +667,7 @@ int w4_moe_select(const w4_rows* logits, int64_t M, int64_t E, const w4_select* 
  * row stride >= D, not overlapping x. ids, weights [M][top_k] as w4_moe_select or w4_moe_route give them;
  * a slot whose id lies outside [0, E) contributes nothing, and a token without any gets
  * y = 0. An expert's weights are read once for a tile of its tokens (8 to 128,
- * by how many an expert gets). Sums are fp32, h and each expert's part of y are
- * rounded to bf16. 0 <= M, M * top_k <= 2^24, top_k <= 32,
+ * by how many an expert gets). Sums are fp32, h is rounded to bf16. 0 <= M, M * top_k <= 2^24, top_k <= 32,
  * E <= 1024. workspace: w4_mx4_moe_workspace_bytes(...) bytes; its contents on entry do not
  * matter. Calls sharing a workspace must not overlap. Deterministic.
  */

@@ -75,7 +75,7 @@ def mx4_moe(gate, up, down, x, ids, weights, act):
     """(y, bound) fp64 [M][D] for fp64 weight stacks, and what y may be off by: sums of K products in fp32 (each of
     at most K additions off by 2^-23 of the sum of magnitudes), h rounded to bf16 (2^-8) after an
     activation whose slope is under 1.13, off by 2^-18 of itself and 2^-22 |g| (1 + tanh cancels
-    for negative g), each expert's part of y and y itself rounded to bf16."""
+    for negative g), and y rounded to bf16."""
     M, D = x.shape
     y, b = np.zeros((M, D)), np.zeros((M, D))
     for m in range(M):
@@ -91,6 +91,5 @@ def mx4_moe(gate, up, down, x, ids, weights, act):
             dh = dh + 2.0 ** -8 * (np.abs(h) + dh)
             y[m] += w * (down[e] @ h)
             s = np.abs(down[e])
-            b[m] += abs(w) * (s @ dh + (F + len(ids[m]) + 2) * 2.0 ** -23 * (s @ (np.abs(h) + dh))
-                             + 2.0 ** -8 * (np.abs(down[e] @ h) + s @ dh))
+            b[m] += abs(w) * (s @ dh + (F + len(ids[m]) + 2) * 2.0 ** -23 * (s @ (np.abs(h) + dh)))
     return y, b + 2.0 ** -8 * (np.abs(y) + b)
