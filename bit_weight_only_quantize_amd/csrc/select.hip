@@ -10,7 +10,7 @@
 // Sorting is k rounds of a wave-wide maximum over 32-bit keys; a lane holds consecutive experts, so the
 // first lane with the maximum has the lowest index. Bound by its dependent steps and instruction issue (920 vector
 // instructions a token): 8192 tokens, 256 experts in
-// 8 groups, top 8, sigmoid with bias: 20 us (27 with everything in 64 bits; 1.7 for the bytes). Finding the k-th key bit by
+// 8 groups, top 8, sigmoid with bias: 18 us (27 with everything in 64 bits; 1.7 for the bytes). Finding the k-th key bit by
 // bit with ballots instead of the rounds, and ranking what it leaves, took 26.
 #include "mx4.hpp"
 #include "topk.hpp"
@@ -99,23 +99,28 @@ __device__ void select_exact(const SelectArgs& a, int64_t m, double* values) {
             if (e < a.E) values[e] = !(l[j] > -INFINITY) ? -INFINITY : p[j] + (a.bias ? (double)a.bias[e] : 0.0);
         }
         wave_lds_sync();
-        double v = 0;
-        if (lane < a.groups) {
-            double b0 = -INFINITY, b1 = -INFINITY;
-            for (int i = 0; i < size; ++i) {
-                const double x = values[lane * size + i];
+        // 1 << share lanes scan a group, then merge their two largest; the first of them speaks for it
+        const int share = 1 << a.share, group = lane >> a.share;
+        double b0 = -INFINITY, b1 = -INFINITY;
+        if (group < a.groups)
+            for (int i = lane & (share - 1); i < size; i += share) {
+                const double x = values[group * size + i];
                 if (x > b0) { b1 = b0; b0 = x; }
                 else if (x > b1) b1 = x;
             }
-            v = a.best == 2 ? b0 + b1 : b0;
+        for (int o = 1; o < share; o *= 2) {
+            const double o0 = __shfl_xor(b0, o, 64), o1 = __shfl_xor(b1, o, 64);
+            b1 = o0 > b0 ? (b0 > o1 ? b0 : o1) : (b1 > o0 ? b1 : o0);
+            b0 = o0 > b0 ? o0 : b0;
         }
-        uint64_t gk = lane < a.groups ? (v > -INFINITY ? order_key(v) : 1) : 0;
+        const double v = a.best == 2 ? b0 + b1 : b0;
+        uint64_t gk = (lane & (share - 1)) == 0 && group < a.groups ? (v > -INFINITY ? order_key(v) : 1) : 0;
         uint64_t kept = 0;
         for (int r = 0; r < a.top_groups; ++r) {
             const uint64_t best = wave_max_u64(gk);
-            const int g = wave_min_dpp(gk == best ? lane : 0x7FFFFFFF);
-            kept |= 1ull << g;
-            if (lane == g) gk = 0;
+            const int at = wave_min_dpp(gk == best ? lane : 0x7FFFFFFF);
+            kept |= 1ull << (at >> a.share);
+            if (lane == at) gk = 0;
         }
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
