@@ -48,11 +48,12 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
     return (act == kActSilu ? g / (1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g)) : gelu_tanh(g)) * u;
 }
 
-// More dynamic LDS than the default 64 KiB for a kernel, up to `most`; asked for once on each device.
-constexpr int kMostLds = 144 << 10;  // beside static arrays of up to 16 KiB
+// More LDS than the default 64 KiB for a kernel with static arrays of up to 16 KiB and `bytes` of dynamic LDS, up to
+// `most` of them; asked for once on each device.
+constexpr int kMostLds = 144 << 10;  // beside such static arrays
 template <typename F>
 inline hipError_t allow_lds(F* kern, int bytes, int most, uint64_t* asked) {
-    if (bytes <= (64 << 10)) return hipSuccess;
+    if (bytes <= (48 << 10)) return hipSuccess;
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;

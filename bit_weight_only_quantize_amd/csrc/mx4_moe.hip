@@ -360,11 +360,12 @@ hipError_t launch_mx4_moe(const Mx4Moe& a, void* work, hipStream_t st) {
     if (way.direct) {
         const dim3 gu((unsigned)((a.F + kDirectWaves - 1) / kDirectWaves), (unsigned)(a.M * a.k));
         const dim3 gd((unsigned)((a.D + kDirectWaves - 1) / kDirectWaves), (unsigned)a.M);
-        const int lds = gemv_lds_bytes((int)a.D);
-    static uint64_t asked;
-    if (const hipError_t e = allow_lds(mx4_gate_up_one_kernel, lds, kMostLds, &asked)) return e;
-        hipLaunchKernelGGL(mx4_gate_up_one_kernel, gu, dim3(64 * kDirectWaves), lds, st, a, h);
-        hipLaunchKernelGGL(mx4_down_one_kernel, gd, dim3(64 * kDirectWaves), gemv_lds_bytes((int)(a.k * a.F)), st, a, h);
+        const int lg = gemv_lds_bytes((int)a.D), ld = gemv_lds_bytes((int)(a.k * a.F));
+        static uint64_t asked_gu, asked_down;
+        if (const hipError_t e = allow_lds(mx4_gate_up_one_kernel, lg, kMostLds, &asked_gu)) return e;
+        if (const hipError_t e = allow_lds(mx4_down_one_kernel, ld, kMostLds, &asked_down)) return e;
+        hipLaunchKernelGGL(mx4_gate_up_one_kernel, gu, dim3(64 * kDirectWaves), lg, st, a, h);
+        hipLaunchKernelGGL(mx4_down_one_kernel, gd, dim3(64 * kDirectWaves), ld, st, a, h);
         return hipGetLastError();
     }
     hipLaunchKernelGGL(mx4_sort_kernel, dim3((unsigned)a.E), dim3(kSortThreads), 0, st, a.ids, (int)(a.M * a.k), a.E, way.rows,

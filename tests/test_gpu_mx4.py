@@ -510,3 +510,27 @@ def test_pair_counts_at_the_borders_between_ways():
             y = w4.mx4_moe(*q, x.cuda(), ids.cuda(), w.cuda()).cpu().double().numpy()
             want, bound = oracle.mx4_moe(*v, x.double().numpy(), ids.numpy(), w.double().numpy(), "gelu_tanh")
             assert (np.abs(y - want) <= bound).all(), (M, e)
+
+
+@pytest.mark.parametrize("M,K", [(1, 24576), (1, 32768), (2, 14336), (9, 3584), (16, 2016)])
+def test_x_at_the_default_size_of_lds(M, K):
+    """X takes 48 to 64 KiB of LDS, beside what the kernels hold for themselves."""
+    wc, ws, wv = integers((50, K), K, 127, 128)
+    xc, xs, xv = integers((M, K), M, 127, 128)
+    want, size = product(xv, wv)
+    assert float(size.max()) < 2 ** 22                   # multiples of 1/4
+    y = w4.mx4_gemm(device(wc, ws), bf16(xv).cuda(), dtype=torch.float32)
+    assert torch.equal(y.cpu().double(), want)
+
+
+@pytest.mark.parametrize("k,F", [(8, 4096), (8, 3104), (32, 1024), (9, 4096)])
+def test_experts_of_one_token_at_the_default_size_of_lds(k, F):
+    E, D = 9, 64
+    q, v = stacks(E, D, F, 31)
+    g = torch.Generator().manual_seed(F)
+    x = torch.randn((1, D), generator=g).to(torch.bfloat16)
+    ids = torch.randint(0, E, (1, k), generator=g, dtype=torch.int32)
+    w = torch.randn((1, k), generator=g)
+    y = w4.mx4_moe(*q, x.cuda(), ids.cuda(), w.cuda()).cpu().double().numpy()
+    want, bound = oracle.mx4_moe(*v, x.double().numpy(), ids.numpy(), w.double().numpy(), "gelu_tanh")
+    assert (np.abs(y - want) <= bound).all()
