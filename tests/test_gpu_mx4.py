@@ -534,3 +534,16 @@ def test_experts_of_one_token_at_the_default_size_of_lds(k, F):
     y = w4.mx4_moe(*q, x.cuda(), ids.cuda(), w.cuda()).cpu().double().numpy()
     want, bound = oracle.mx4_moe(*v, x.double().numpy(), ids.numpy(), w.double().numpy(), "gelu_tanh")
     assert (np.abs(y - want) <= bound).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(4096, 4096, 160), (2048, 11008, 96), (2048, 4096, 96), (4097, 257, 224), (513, 8000, 352),
+                                   (1000, 1000, 4128)])
+@pytest.mark.parametrize("x4", [False, True])
+def test_product_in_every_block(M, N, K, x4):
+    """Sizes at which the large blocks of the plan are taken, exact as above."""
+    wc, ws, wv = integers((N, K), 1)
+    xc, xs, xv = integers((M, K), 2)
+    want, size = product(xv, wv)
+    assert float(size.max()) < 2 ** 20
+    y = w4.mx4_gemm(device(wc, ws), device(xc, xs) if x4 else bf16(xv).cuda(), dtype=torch.float32)
+    assert torch.equal(y.cpu().double(), want)

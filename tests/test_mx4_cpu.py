@@ -133,3 +133,17 @@ def test_experts_refuse():
     assert call(ws=None) == -5 and call(wb=need - 1) == -5 and call(ws=8) == -3
     assert L.w4_mx4_moe_workspace_bytes(0, 2, E, D, F) == 0
     assert L.w4_mx4_moe_workspace_bytes(1 << 24, 2, E, D, F) == 0
+
+
+def test_workspaces_of_all_kinds_of_sizes():
+    """Host-only: every plan has a size, whole blocks of fp32 sums for each piece of K, 0 for up to 16 rows."""
+    pieces = set()
+    for x4 in (0, 1):
+        for N in (1, 129, 1000, 4096, 11008, 152064):
+            for K in (32, 992, 4096, 11008, 65536):
+                for M in (1, 16, 17, 64, 100, 128, 129, 200, 256, 300, 512, 1000, 4097):
+                    n = L.w4_mx4_gemm_workspace_bytes(mat(N, K), M, x4)
+                    assert n % (64 * 128 * 4) == 0 and (M > 16 or n == 0), (x4, N, K, M)
+                    assert n <= 16 * 4 * (M + 255) * (N + 255)
+                    pieces.add((x4, n > 0))
+    assert len(pieces) == 4
