@@ -56,7 +56,8 @@ __device__ __forceinline__ float logit(const SelectArgs& a, int64_t m, int e) {
     return BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
 }
 
-// A token with everything in 64 bits; lane holds the experts lane + 64 j. values: [64 EPL] in LDS.
+// A token with everything in 64 bits; lane holds the experts lane + 64 j. values: [64 EPL] in LDS. NaN logits
+// count as masked, so that they stay out of the softmax's sum.
 template <int EPL, bool BF16>
 __device__ void select_exact(const SelectArgs& a, int64_t m, double* values) {
     const int lane = threadIdx.x & 63;
@@ -66,7 +67,7 @@ __device__ void select_exact(const SelectArgs& a, int64_t m, double* values) {
     for (int j = 0; j < EPL; ++j) {
         const int e = lane + 64 * j;
         const float v = logit<BF16>(a, m, min(e, a.E - 1));
-        l[j] = e < a.E ? v : -INFINITY;
+        l[j] = e < a.E && v == v ? v : -INFINITY;
         mx = fmaxf(mx, l[j]);
     }
     mx = wave_max_dpp(mx);
