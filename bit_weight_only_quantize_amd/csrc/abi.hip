@@ -986,7 +986,7 @@ int w4_kv_attention(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4
 }
 
 // ---------------------------------------------------------------- microscaled 4-bit
-// Rows (a launch holds under 2^32 threads, up to 64 a row) and columns (bytes of 16 rows in 31 bits)
+// Rows and columns (bytes of 16 rows in 31 bits)
 static const int64_t kMxRows = 1 << 26, kMxColumns = 1 << 24;
 
 // One matrix, or a stack of any number of them (experts == 0)

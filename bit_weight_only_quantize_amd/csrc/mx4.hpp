@@ -48,6 +48,9 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
     return (act == kActSilu ? g / (1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g)) : gelu_tanh(g)) * u;
 }
 
+// A launch holds under 2^32 threads.
+inline bool launchable(int64_t blocks, int threads) { return blocks <= 0xffffffffLL / threads; }
+
 // More LDS than the default 64 KiB for a kernel with static arrays of up to 16 KiB and `bytes` of dynamic LDS, up to
 // `most` of them; asked for once on each device.
 constexpr int kMostLds = 144 << 10;  // beside such static arrays

@@ -29,6 +29,7 @@ __global__ __launch_bounds__(64 * kGemvWaves) void mx4_gemv_kernel(Mx4Mat W, con
 }
 
 static constexpr int64_t kGemvMaxK = 65536;  // x in LDS: 128 KiB
+static constexpr int64_t kGemvMaxN = 0xffffffffLL / (64 * kGemvWaves) * kGemvWaves;  // under 2^32 threads
 
 static hipError_t launch_gemv1(const Mx4Mat& W, const uint16_t* x, void* Y, bool y_bf16, hipStream_t st) {
     const int lds = gemv_lds_bytes((int)W.K);
@@ -295,7 +296,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_block_sum_kernel(BlockArgs a
 template <bool X4, int BM, int BN, int WM, int WN>
 static hipError_t launch_block(BlockArgs a, hipStream_t st) {
     const int64_t tm = (a.M + BM - 1) / BM, tn = (a.W.N + BN - 1) / BN;
-    if (tm * tn * a.parts > 0xffffffffLL / (64 * WM * WN) - 8) return hipErrorInvalidValue;  // threads of a launch
+    if (!launchable((tm * tn * a.parts + 7) / 8 * 8, 64 * WM * WN)) return hipErrorInvalidValue;
     a.tiles_n = (int)tn;
     a.tiles = (int)(tm * tn);
     const int lds = kStages * (X4 ? mx4_stage_bytes_x4<BM, BN>() : mx4_stage_bytes<BM, BN>());
@@ -390,7 +391,7 @@ hipError_t launch_mx4_gemm(const Mx4Mat& W, const Mx4X& X, int64_t M, void* Y, b
         const BlockArgs a = {W, X, M, Y, y_stride, y_bf16, 0, 0, p.parts, (float*)work};
         return X.x ? launch_blocks<false>(p.shape, a, st) : launch_blocks<true>(p.shape, a, st);
     }
-    if (X.x && M == 1 && W.K <= kGemvMaxK) return launch_gemv1(W, X.x, Y, y_bf16, st);
+    if (X.x && M == 1 && W.K <= kGemvMaxK && W.N <= kGemvMaxN) return launch_gemv1(W, X.x, Y, y_bf16, st);
     if (X.x) return launch_few(W, X, M, Y, y_bf16, y_stride, st);
     hipLaunchKernelGGL(mx4_few_x4_kernel, dim3((unsigned)((W.N + 31) / 32)), dim3(256), 0, st, W, X, (int)M, Y, y_bf16,
                        y_stride);

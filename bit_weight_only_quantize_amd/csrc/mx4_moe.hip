@@ -305,6 +305,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_moe_block_kernel(Mx4Moe a
 }
 
 // ---------------------------------------------------------------- a token's parts
+constexpr int64_t kCombineMost = 1 << 23;  // tokens of a launch, 256 threads each
 __global__ __launch_bounds__(256) void mx4_combine_kernel(Mx4Moe a, const int32_t* __restrict__ place,
                                                           const float* __restrict__ part) {
     const int64_t m = blockIdx.x;
@@ -350,7 +351,11 @@ static hipError_t launch_moe_block(const Mx4Moe& a, int64_t slots, const int4* t
 hipError_t launch_mx4_moe(const Mx4Moe& a, void* work, hipStream_t st) {
     const Mx4MoeWork L = moe_layout(a.M, a.k, a.E, a.D, a.F);
     const MoeWay way = moe_way(a.M, a.k, a.E, a.D, a.F);
-    if (L.slots * ((a.D > a.F ? a.D : a.F) / 64 + 1) > 0xffffffffLL / 512) return hipErrorInvalidValue;  // threads of a launch
+    // columns of a workgroup of the gate/up and of the down product, and threads, as launched below
+    const int gu_cols = way.rows == 64 ? 128 : 64, down_cols = 2 * gu_cols, down_threads = way.rows <= 16 ? 512 : 256;
+    if (!launchable(L.slots * ((a.F + gu_cols - 1) / gu_cols), 256) ||
+        !launchable(L.slots * ((a.D + down_cols - 1) / down_cols), down_threads))
+        return hipErrorInvalidValue;  // before the first launch
     uint8_t* base = (uint8_t*)work;
     int4* tiles = (int4*)(base + L.tiles);
     int32_t* pairs = (int32_t*)(base + L.pairs);
@@ -391,7 +396,13 @@ hipError_t launch_mx4_moe(const Mx4Moe& a, void* work, hipStream_t st) {
                                  : blocks(launch_moe_block<true, 128, 128, 2, 2>, launch_moe_block<false, 128, 128, 2, 2>);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(mx4_combine_kernel, dim3((unsigned)a.M), dim3(256), 0, st, a, place, part);
+    for (int64_t m = 0; m < a.M; m += kCombineMost) {
+        Mx4Moe b = a;
+        b.weights += m * a.k;
+        b.y += m * a.y_stride;
+        hipLaunchKernelGGL(mx4_combine_kernel, dim3((unsigned)(a.M - m < kCombineMost ? a.M - m : kCombineMost)), dim3(256),
+                           0, st, b, place + m * a.k, part);
+    }
     return hipGetLastError();
 }
 

@@ -329,6 +329,17 @@ hipError_t launch_moe_select(SelectArgs a, bool bf16, hipStream_t st) {
     a.size = a.E / a.groups;
     a.share = 0;
     while (2 * (a.groups << a.share) <= 64) ++a.share;
+    constexpr int64_t kMost = 1 << 25;  // tokens of a launch, 64 threads each
+    if (a.M > kMost) {
+        SelectArgs b = a;
+        b.M = kMost;
+        if (const hipError_t e = launch_moe_select(b, bf16, st)) return e;
+        b.M = a.M - kMost;
+        b.logits = static_cast<const char*>(a.logits) + kMost * a.row_stride * (bf16 ? 2 : 4);
+        b.ids += kMost * a.k;
+        b.weights += kMost * a.k;
+        return launch_moe_select(b, bf16, st);
+    }
     const dim3 grid((unsigned)((a.M + kSelectWaves - 1) / kSelectWaves)), block(64 * kSelectWaves);
 #define W4_SELECT(EPL)                                                                                   \
     if (a.E <= 64 * EPL) {                                                                               \
