@@ -48,6 +48,17 @@ __device__ __forceinline__ float gated(float g, float u, int act) {
     return (act == kActSilu ? g / (1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g)) : gelu_tanh(g)) * u;
 }
 
+// A row of values kept to 16 bits, as two bf16 pieces: each value's nearest bf16 number and that of the rest. Group g of
+// 32 values lies at 64 g, its first pieces, then its second ones, so that a product over a row's 2 K pieces is
+// one over K values with every group of W taken twice.
+__device__ __forceinline__ void store_pieces(uint16_t* row, int64_t k, float v) {
+    const uint16_t hi = to_bf16(v);
+    const float f = __uint_as_float((uint32_t)hi << 16);
+    uint16_t* p = row + k + (k & ~(int64_t)(kMxGroup - 1));
+    p[0] = hi;
+    p[kMxGroup] = fabsf(f) < INFINITY ? to_bf16(v - f) : (uint16_t)0;
+}
+
 // A launch holds under 2^32 threads.
 inline bool launchable(int64_t blocks, int threads) { return blocks <= 0xffffffffLL / threads; }
 

@@ -51,18 +51,21 @@ __device__ __forceinline__ void loads_done_barrier() {
 __device__ const __align__(16) uint16_t kMx4Zeros[8] = {};
 
 constexpr int kBlockK = 64, kStages = 4;
-template <int BM, int BN>
-constexpr int mx4_stage_bytes() { return BM * kBlockK * 2 + BN * kBlockK / 2; }
+template <int BM, int BN, bool PIECES = false>
+constexpr int mx4_stage_bytes() { return BM * kBlockK * 2 + BN * kBlockK / (PIECES ? 4 : 2); }
 
 // The k loop. xrow(r): row r (0 .. BM - 1) of the block, any valid row where it has none; wcol(c):
-// the same for W as {codes, scales} of column c. Steps t0 .. t1 - 1. acc: of the wavefront's tiles.
-template <int BM, int BN, int WM, int WN, typename XRow, typename WCol>
+// the same for W as {codes, scales} of column c. Steps t0 .. t1 - 1. acc: of the wavefront's tiles. PIECES: X holds
+// pieces (store_pieces), so a step is one group of W, and an operand of W meets both pieces: slice kk of lane half h takes
+// piece kk % 2 of the k of code word 2h + kk / 2.
+template <int BM, int BN, int WM, int WN, bool PIECES = false, typename XRow, typename WCol>
 __device__ __forceinline__ void mx4_block_product(uint8_t* lds, XRow xrow, WCol wcol, int K, int t0, int t1,
                                                   f32x16_t (&acc)[BM / WM / 32][BN / WN / 32]) {
     constexpr int NW = WM * WN, NI = BM / WM / 32, NJ = BN / WN / 32;
-    constexpr int XL = BM / 8 / NW, CL = BN / 32;  // direct loads of a step: X per wavefront, codes in all
-    static_assert(BM % (8 * NW) == 0 && BN % 32 == 0 && (CL % NW == 0 || CL < NW), "loads per wavefront");
-    constexpr int X_BYTES = BM * kBlockK * 2, STAGE = mx4_stage_bytes<BM, BN>();
+    constexpr int PER = PIECES ? 1 : 2;  // groups of a step
+    constexpr int XL = BM / 8 / NW, CC = 64 / PER, CL = BN / CC;  // direct loads of a step: X per wavefront, codes in all
+    static_assert(BM % (8 * NW) == 0 && BN % CC == 0 && (CL % NW == 0 || CL < NW), "loads per wavefront");
+    constexpr int X_BYTES = BM * kBlockK * 2, STAGE = mx4_stage_bytes<BM, BN, PIECES>();
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN, half = lane >> 5, l32 = lane & 31;
@@ -76,18 +79,18 @@ __device__ __forceinline__ void mx4_block_product(uint8_t* lds, XRow xrow, WCol 
     constexpr int CW = CL >= NW ? CL / NW : 1;
     const uint8_t* csrc[CW];
 #pragma unroll
-    for (int i = 0; i < CW; ++i) csrc[i] = wcol(32 * (min(wave, CL - 1) * CW + i) + l32).codes;
+    for (int i = 0; i < CW; ++i) csrc[i] = wcol(CC * (min(wave, CL - 1) * CW + i) + lane % CC).codes;
     const uint8_t* ssrc[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) ssrc[j] = wcol(wn * (BN / WN) + 32 * j + l32).scale;
-    const int groups = K / kMxGroup;
+    const int groups = K / kMxGroup, own = PIECES ? 0 : half;
 
     // A column's scale bytes for the kStages steps from t on, in 8 bytes (a lane load of single
     // bytes touches 32 lines a step, as many as all else); past the end of a row, its last ones.
     uint64_t sb[NJ];
     auto load_scales = [&](int t) {
         if (groups >= 2 * kStages) {
-            const int g = min(2 * t, groups - 2 * kStages);
+            const int g = min(PER * t, groups - 2 * kStages);
 #pragma unroll
             for (int j = 0; j < NJ; ++j) __builtin_memcpy(&sb[j], ssrc[j] + g, 8);
         } else {
@@ -99,14 +102,14 @@ __device__ __forceinline__ void mx4_block_product(uint8_t* lds, XRow xrow, WCol 
         }
     };
     auto scale_of = [&](uint64_t v, int t, int i) {  // step t + i of the bytes loaded for step t
-        const int g = groups >= 2 * kStages ? min(2 * t, groups - 2 * kStages) : 0;
-        return mx4_scale((uint32_t)(v >> (8 * (min(2 * (t + i) + half, groups - 1) - g))) & 255u);
+        const int g = groups >= 2 * kStages ? min(PER * t, groups - 2 * kStages) : 0;
+        return mx4_scale((uint32_t)(v >> (8 * (min(PER * (t + i) + own, groups - 1) - g))) & 255u);
     };
     auto issue = [&](int t, int stage) {
         t = min(t, t1 - 1);  // past the end: a step again, into a stage nobody reads
         uint8_t* st = lds + stage * STAGE;
-        const int g = min(2 * t + half, groups - 1);
-        if (2 * t + 1 < groups) {
+        const int g = min(PER * t + own, groups - 1);
+        if (PIECES || 2 * t + 1 < groups) {
 #pragma unroll
             for (int i = 0; i < XL; ++i)
                 __builtin_amdgcn_global_load_lds((gbl_void*)(xsrc[i] + kBlockK * t),
@@ -118,16 +121,17 @@ __device__ __forceinline__ void mx4_block_product(uint8_t* lds, XRow xrow, WCol 
                                                  (lds_void*)(st + (XL * wave + i) * 1024), 16, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < CW; ++i)  // (wavefronts past the last 32 columns fetch those again)
+        for (int i = 0; i < CW; ++i)  // (wavefronts past the last columns fetch those again)
             __builtin_amdgcn_global_load_lds((gbl_void*)(csrc[i] + 16 * g),
                                              (lds_void*)(st + X_BYTES + (min(wave, CL - 1) * CW + i) * 1024), 16, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
     };
     int aoff[4];  // of this lane's chunk of slice kk in row l32 of a tile
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) aoff[kk] = (wm * (BM / WM) + l32) * 128 + (((4 * half + kk) ^ ((l32 >> 1) & 7)) << 4);
+    for (int kk = 0; kk < 4; ++kk) aoff[kk] = (wm * (BM / WM) + l32) * 128 + (((PIECES ? 4 * (kk & 1) + 2 * half + (kk >> 1) : 4 * half + kk) ^ ((l32 >> 1) & 7)) << 4);
     bf16x8_t a[2][NI], b[2][NJ];
-    u32x4_t cw[NJ];
+    typedef unsigned Codes __attribute__((ext_vector_type(4 / (3 - PER))));  // of a lane and column in a step
+    Codes cw[NJ];
     float sw[NJ];
     auto load_a = [&](int stage, int kk) {
 #pragma unroll
@@ -136,19 +140,24 @@ __device__ __forceinline__ void mx4_block_product(uint8_t* lds, XRow xrow, WCol 
     };
     auto load_codes = [&](int stage) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            cw[j] = *reinterpret_cast<const u32x4_t*>(lds + stage * STAGE + X_BYTES + (wn * NJ + j) * 1024 + lane * 16);
+        for (int j = 0; j < NJ; ++j) {
+            const uint8_t* p = lds + stage * STAGE + X_BYTES;
+            if constexpr (PIECES) cw[j] = *reinterpret_cast<const Codes*>(p + (wn * NJ + j) * 512 + l32 * 16 + half * 8);
+            else cw[j] = *reinterpret_cast<const Codes*>(p + (wn * NJ + j) * 1024 + lane * 16);
+        }
     };
     auto unpack = [&](int kk) {
+        if (PIECES && (kk & 1)) return;  // both pieces' slices share it
+        const int w = PIECES ? kk >> 1 : kk;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) b[kk & 1][j] = mx4_to_bf16(cw[j][kk], sw[j]);
+        for (int j = 0; j < NJ; ++j) b[w & 1][j] = mx4_to_bf16(cw[j][w], sw[j]);
     };
     auto products = [&](int kk, int reads) {
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[kk & 1][i], b[kk & 1][j], acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[kk & 1][i], b[(PIECES ? kk >> 1 : kk) & 1][j], acc[i][j], 0, 0, 0);
 #pragma unroll
         for (int r = 0; r < NI * NJ; ++r) {
             __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);  // a matrix instruction

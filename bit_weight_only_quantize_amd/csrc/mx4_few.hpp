@@ -93,21 +93,30 @@ struct FewStream {
                 sc[t][h] = ws[t][h][at];
             }
     }
-    // load(first) has been called. x: this lane's row of X in LDS, at byte 64 g
+    // load(first) has been called. x: this lane's row of X in LDS, at byte 64 g; for P = 2 pieces of X (store_pieces), staged
+    // as steps of twice as many values, at 128 g
+    template <int P = 1>
     __device__ __forceinline__ void run(const uint8_t* x, int first, int by, int end, int s0, FewSums (&acc)[RT]) {
         for (int s = first; s < end; s += by) {
-            const uint8_t* p = x + 2 * kFewK * (s - s0);
+            const uint8_t* p = x + 2 * kFewK * P * (s - s0);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bf16x8_t a0 = *reinterpret_cast<const bf16x8_t*>(p + 16 * j);
-                const bf16x8_t a1 = *reinterpret_cast<const bf16x8_t*>(p + kFewK + 16 * j);
+                bf16x8_t a[P][2];  // [piece][half of the step]
+#pragma unroll
+                for (int q = 0; q < P; ++q)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        a[q][i] = *reinterpret_cast<const bf16x8_t*>(p + kFewK * P * i + 2 * kMxGroup * q + 16 * j);
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const bf16x8_t b = mx4_to_bf16(w[t][h][j], mx4_scale(sc[t][h]));
-                        acc[t].v[h][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, b, acc[t].v[h][0], 0, 0, 0);
-                        acc[t].v[h][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b, acc[t].v[h][1], 0, 0, 0);
+#pragma unroll
+                        for (int q = 0; q < P; ++q)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                acc[t].v[h][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[q][i], b, acc[t].v[h][i], 0, 0, 0);
                     }
             }
             __builtin_amdgcn_sched_barrier(0);

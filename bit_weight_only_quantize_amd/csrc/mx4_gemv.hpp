@@ -14,15 +14,16 @@
 namespace w4 {
 
 __host__ __device__ inline int gemv_vectors(int K) { return (K / kMxGroup + 63) / 64 * 64; }
-__host__ __device__ inline int gemv_lds_bytes(int K) { return 64 * gemv_vectors(K); }
+__host__ __device__ inline int gemv_lds_bytes(int K) { return 64 * gemv_vectors(K); }  // a piece
 
-// By all threads of the workgroup
+// By all threads of the workgroup. P = 2 pieces of x (store_pieces): eight planes, the second pieces' behind the first ones'.
+template <int P = 1>
 __device__ __forceinline__ void gemv_stage(uint8_t* lds, const uint16_t* x, int K) {
     const int V = gemv_vectors(K);
-    for (int i = threadIdx.x; i < 4 * V; i += blockDim.x) {
+    for (int i = threadIdx.x; i < 4 * P * V; i += blockDim.x) {
         u32x4_t v = {0, 0, 0, 0};
-        if (8 * i < K) v = *reinterpret_cast<const u32x4_t*>(x + 8 * i);
-        *reinterpret_cast<u32x4_t*>(lds + (i & 3) * (16 * V) + (i >> 2) * 16) = v;
+        if (8 * i < P * K) v = *reinterpret_cast<const u32x4_t*>(x + 8 * i);
+        *reinterpret_cast<u32x4_t*>(lds + i % (4 * P) * (16 * V) + i / (4 * P) * 16) = v;
     }
 }
 

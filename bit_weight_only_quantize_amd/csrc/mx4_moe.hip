@@ -1,6 +1,10 @@
 // The gated FFN of each token's chosen experts, with microscaled 4-bit weights:
-//   y[m] = sum_j weights[m][j] W_down[e] h,  h = bf16(act(W_gate[e] x[m]) * (W_up[e] x[m])),  e = ids[m][j].
+//   y[m] = sum_j weights[m][j] W_down[e] h,  h = act(W_gate[e] x[m]) * (W_up[e] x[m]),  e = ids[m][j].
 //
+// h is kept to 16 bits, two bf16 pieces a value, which the down product multiplies one after the other: with a single
+// piece its rounding was most of what results were off by (2.4e-3 of 64 bits in norm, 1.7e-3 with two, which is the
+// rounding of y). The second piece took 4096 tokens from 520 us to 604 (645 with every operand of W unpacked for each piece), 61
+// tokens from 112 to 116, one token nothing.
 // Pair p = m k + j. Three ways, by the number of pairs and of pairs an expert gets:
 //   * few pairs (kDirectPairs): each pair's gate and up rows by the one-row kernel, then a token's
 //     y in one pass over its experts' down rows. Two launches, no sorting.
@@ -33,7 +37,9 @@ constexpr int64_t kDirectPairs = 16;
 static MoeWay moe_way(int64_t M, int k, int64_t E, int64_t D, int64_t F) {
     const int64_t P = M * k;
     if (P <= kDirectPairs && k * F <= (32 << 10) && D <= (64 << 10)) return {true, 0};
-    const int64_t each = P / E, room = kMostLds / (2 * (D > F ? D : F) + 2 * kFewK + 16);  // rows that fit in LDS
+    // rows that fit in LDS, of x and of pieces of h
+    const int steps = few_steps(D) > 2 * few_steps(F) ? few_steps(D) : 2 * few_steps(F);
+    const int64_t each = P / E, room = kMostLds / few_row_bytes(steps);
     if (each <= 6 && room >= 8) return {false, 8};
     if (each <= 16 && room >= 16) return {false, 16};
     return {false, each <= 320 ? 64 : 128};
@@ -49,7 +55,7 @@ static Mx4MoeWork moe_layout(int64_t M, int k, int64_t E, int64_t D, int64_t F) 
     L.pairs = up((size_t)L.slots * 16);
     L.place = L.pairs + (way.direct ? 0 : up((size_t)P * 4));
     L.h = L.place + (way.direct ? 0 : up((size_t)P * 4));
-    L.part = L.h + up((size_t)P * F * 2);
+    L.part = L.h + up((size_t)P * F * 4);
     L.total = L.part + (size_t)P * D * 4;
     return L;
 }
@@ -60,7 +66,7 @@ size_t mx4_moe_workspace(int64_t M, int k, int64_t E, int64_t D, int64_t F) {
 // ---------------------------------------------------------------- few pairs
 constexpr int kDirectWaves = 8;
 
-// h[p][f] of pair blockIdx.y: a gate and an up row a wavefront
+// Pieces of h of pair blockIdx.y: a gate and an up row a wavefront
 __global__ __launch_bounds__(64 * kDirectWaves) void mx4_gate_up_one_kernel(Mx4Moe a, uint16_t* __restrict__ h) {
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -78,7 +84,7 @@ __global__ __launch_bounds__(64 * kDirectWaves) void mx4_gate_up_one_kernel(Mx4M
     gemv_stage(lds, a.x + (p / a.k) * a.x_stride, D);
     __syncthreads();
     s.finish(lds, gemv_vectors(D), acc);
-    if (lane == 0 && f < a.F) h[(int64_t)p * a.F + f] = to_bf16(gated(acc[0], acc[1], a.act));
+    if (lane == 0 && f < a.F) store_pieces(h + 2 * p * a.F, f, gated(acc[0], acc[1], a.act));
 }
 
 // y[m][d] of token blockIdx.y, a wavefront a d: the rows d of the token's k experts as one row of k F
@@ -98,7 +104,7 @@ __global__ __launch_bounds__(64 * kDirectWaves) void mx4_down_one_kernel(Mx4Moe 
         wts[threadIdx.x] = in ? a.weights[m * a.k + threadIdx.x] : 0.f;
     }
     // h of a slot without an expert was never written: its vectors are left out below
-    gemv_stage(lds, h + m * a.k * F, a.k * F);
+    gemv_stage<2>(lds, h + 2 * m * a.k * F, a.k * F);
     __syncthreads();
     float acc = 0.f;
     constexpr int U = 4;
@@ -123,10 +129,13 @@ __global__ __launch_bounds__(64 * kDirectWaves) void mx4_down_one_kernel(Mx4Moe 
             float dot = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const u32x4_t x = *reinterpret_cast<const u32x4_t*>(lds + j * (16 * V) + (v0 + 64 * u + lane) * 16);
                 const u32x4_t b = __builtin_bit_cast(u32x4_t, mx4_to_bf16(w[u][j], f));
 #pragma unroll
-                for (int q = 0; q < 4; ++q) dot = dot2_bf16(b[q], x[q], dot);
+                for (int s = 0; s < 2; ++s) {
+                    const u32x4_t x = *reinterpret_cast<const u32x4_t*>(lds + (j + 4 * s) * (16 * V) + (v0 + 64 * u + lane) * 16);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) dot = dot2_bf16(b[q], x[q], dot);
+                }
             }
             if (in[u]) acc = fmaf(wt[u], dot, acc);
         }
@@ -225,6 +234,7 @@ __global__ __launch_bounds__(64 * NW) void mx4_moe_few_kernel(Mx4Moe a, const in
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t N = GU ? a.F : a.D, n0 = ((int64_t)block * NW + wave) * 16;
+    constexpr int P = GU ? 1 : 2;  // pieces of a value of x or h
     const int K = (int)(GU ? a.D : a.F), steps = few_steps(K);
     FewStream<RT> f;
     f.groups = K / kMxGroup;
@@ -239,20 +249,20 @@ __global__ __launch_bounds__(64 * NW) void mx4_moe_few_kernel(Mx4Moe a, const in
 #pragma unroll
     for (int i = 0; i < RT; ++i) acc[i].clear();
     f.load(0);
-    few_stage(lds, [&](int r) { return GU ? a.x + (pairs[t.y + r] / a.k) * a.x_stride : h + (int64_t)(t.y + r) * K; }, t.z, K,
-              0, steps);
+    few_stage(lds, [&](int r) { return GU ? a.x + (pairs[t.y + r] / a.k) * a.x_stride : h + (int64_t)(t.y + r) * (P * K); }, t.z,
+              P * K, 0, P * steps);
     __syncthreads();
     if (n0 >= N) return;
-    f.run(lds + min(c, t.z - 1) * few_row_bytes(steps) + 64 * g, 0, 1, steps, 0, acc);
+    f.template run<P>(lds + min(c, t.z - 1) * few_row_bytes(P * steps) + 64 * P * g, 0, 1, steps, 0, acc);
     const int64_t n = n0 + few_row(c);
     if (n >= N) return;
     const f32x4_t v = acc[0].rows(), u = acc[RT - 1].rows();
 #pragma unroll
     for (int r = 0; r < 4; ++r)
         if (4 * g + r < t.z) {
-            const int64_t at = (int64_t)(t.y + 4 * g + r) * N + n;
-            if constexpr (GU) h[at] = to_bf16(gated(v[r], u[r], a.act));
-            else part[at] = v[r];
+            const int64_t row = t.y + 4 * g + r;
+            if constexpr (GU) store_pieces(h + row * 2 * N, n, gated(v[r], u[r], a.act));
+            else part[row * N + n] = v[r];
         }
 }
 
@@ -277,14 +287,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_moe_block_kernel(Mx4Moe a
         for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16_t{};
     const auto xrow = [&](int r) -> const uint16_t* {
         const int p = t.y + min(r, t.z - 1);
-        return GU ? a.x + (pairs[p] / a.k) * a.x_stride : h + (int64_t)p * K;
+        return GU ? a.x + (pairs[p] / a.k) * a.x_stride : h + (int64_t)p * (2 * K);
     };
     const auto wcol = [&](int c) {
         const Mx4Mat& w = !GU ? a.down : (c / 32) & 1 ? a.up : a.gate;
         const int64_t n = (int64_t)t.x * N + min(n0 + (GU ? c / 64 * 32 + c % 32 : c), N - 1);
         return Mx4Mat{w.codes + n * (K / 2), w.scale + n * (K / 32), 0, 0};
     };
-    mx4_block_product<BM, BN, WM, WN>(lds, xrow, wcol, K, 0, (K + kBlockK - 1) / kBlockK, acc);
+    mx4_block_product<BM, BN, WM, WN, !GU>(lds, xrow, wcol, K, 0, GU ? (K + kBlockK - 1) / kBlockK : K / kMxGroup, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int row = (wave / WN) * (BM / WM) + 4 * (lane >> 5);
     const int64_t n = n0 + (wave % WN) * (GU ? 32 : 64) + (lane & 31);
@@ -296,7 +306,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mx4_moe_block_kernel(Mx4Moe a
             if (m >= t.z) continue;
             const int64_t at = (int64_t)(t.y + m) * N + n;
             if constexpr (GU) {
-                if (n < N) h[at] = to_bf16(gated(acc[i][0][r], acc[i][1][r], a.act));
+                if (n < N) store_pieces(h + (int64_t)(t.y + m) * 2 * N, n, gated(acc[i][0][r], acc[i][1][r], a.act));
             } else {
                 if (n < N) part[at] = acc[i][0][r];
                 if (n + 32 < N) part[at + 32] = acc[i][1][r];
@@ -340,7 +350,7 @@ template <bool GU, int BM, int BN, int WM, int WN>
 static hipError_t launch_moe_block(const Mx4Moe& a, int64_t slots, const int4* tiles, const int32_t* pairs, uint16_t* h,
                                    float* part, hipStream_t st) {
     const int64_t N = GU ? a.F : a.D;
-    const int lds = kStages * mx4_stage_bytes<BM, BN>(), cols = GU ? BN / 2 : BN, nb = (int)((N + cols - 1) / cols);
+    const int lds = kStages * mx4_stage_bytes<BM, BN, !GU>(), cols = GU ? BN / 2 : BN, nb = (int)((N + cols - 1) / cols);
     auto kern = mx4_moe_block_kernel<GU, BM, BN, WM, WN>;
     static uint64_t asked;
     if (const hipError_t e = allow_lds(kern, lds, lds, &asked)) return e;
@@ -365,7 +375,7 @@ hipError_t launch_mx4_moe(const Mx4Moe& a, void* work, hipStream_t st) {
     if (way.direct) {
         const dim3 gu((unsigned)((a.F + kDirectWaves - 1) / kDirectWaves), (unsigned)(a.M * a.k));
         const dim3 gd((unsigned)((a.D + kDirectWaves - 1) / kDirectWaves), (unsigned)a.M);
-        const int lg = gemv_lds_bytes((int)a.D), ld = gemv_lds_bytes((int)(a.k * a.F));
+        const int lg = gemv_lds_bytes((int)a.D), ld = 2 * gemv_lds_bytes((int)(a.k * a.F));
         static uint64_t asked_gu, asked_down;
         if (const hipError_t e = allow_lds(mx4_gate_up_one_kernel, lg, kMostLds, &asked_gu)) return e;
         if (const hipError_t e = allow_lds(mx4_down_one_kernel, ld, kMostLds, &asked_down)) return e;
@@ -378,7 +388,7 @@ hipError_t launch_mx4_moe(const Mx4Moe& a, void* work, hipStream_t st) {
     if (way.rows <= 16) {
         constexpr int GW = 4, DW = 8;
         const int nf = (int)((a.F + 16 * GW - 1) / (16 * GW)), nd = (int)((a.D + 16 * DW - 1) / (16 * DW));
-        const int lg = way.rows * few_row_bytes(few_steps(a.D)), ld = way.rows * few_row_bytes(few_steps(a.F));
+        const int lg = way.rows * few_row_bytes(few_steps(a.D)), ld = way.rows * few_row_bytes(2 * few_steps(a.F));
         auto gu = mx4_moe_few_kernel<true, GW>;
         auto down = mx4_moe_few_kernel<false, DW>;
         static uint64_t asked_gu, asked_down;

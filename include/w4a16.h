@@ -661,13 +661,13 @@ int w4_moe_select(const w4_rows* logits, int64_t M, int64_t E, const w4_select* 
  * Mixture-of-experts FFN with microscaled 4-bit weights, for one token up to long
  * prompts:
  *   y[m] = sum_j weights[m][j] * W_down[e] h,
- *   h = bf16(act(W_gate[e] x[m]) * (W_up[e] x[m])),   e = ids[m][j],
+ *   h = act(W_gate[e] x[m]) * (W_up[e] x[m]),   e = ids[m][j],
  * with act gelu_tanh (W4_ACT_GELU_TANH, as everywhere above) or silu. gate, up: stacks
  * [E][F][D]; down [E][D][F]; D and F multiples of 32. x bf16 [M][D]; y bf16 [M][D] with a
  * row stride >= D, not overlapping x. ids, weights [M][top_k] as w4_moe_select or w4_moe_route give them;
  * a slot whose id lies outside [0, E) contributes nothing, and a token without any gets
  * y = 0. An expert's weights are read once for a tile of its tokens (8 to 128,
- * by how many an expert gets). Sums are fp32, h is rounded to bf16. 0 <= M, M * top_k <= 2^24, top_k <= 32,
+ * by how many an expert gets). Sums are fp32, h is kept to 16 bits (two bf16 numbers). 0 <= M, M * top_k <= 2^24, top_k <= 32,
  * E <= 1024. workspace: w4_mx4_moe_workspace_bytes(...) bytes; its contents on entry do not
  * matter. Calls sharing a workspace must not overlap. Deterministic.
  */

@@ -73,7 +73,7 @@ def gated(g, u, act):
 
 def mx4_moe(gate, up, down, x, ids, weights, act):
     """(y, bound) fp64 [M][D] for fp64 weight stacks, and what y may be off by: sums of K products in fp32 (each of
-    at most K additions off by 2^-23 of the sum of magnitudes), h rounded to bf16 (2^-8) after an
+    at most K additions off by 2^-23 of the sum of magnitudes), h rounded to 16 bits (2^-16) after an
     activation whose slope is under 1.13, off by 2^-18 of itself and 2^-22 |g| (1 + tanh cancels
     for negative g), and y rounded to bf16."""
     M, D = x.shape
@@ -88,7 +88,7 @@ def mx4_moe(gate, up, down, x, ids, weights, act):
             h = gated(g, u, act)
             a = np.abs(gated(g, np.ones(F), act))
             dh = 1.13 * tg * (np.abs(u) + tu) + a * tu + 2.0 ** -18 * np.abs(h) + 2.0 ** -22 * np.abs(g * u)
-            dh = dh + 2.0 ** -8 * (np.abs(h) + dh)
+            dh = dh + 2.0 ** -16 * (np.abs(h) + dh)
             y[m] += w * (down[e] @ h)
             s = np.abs(down[e])
             b[m] += abs(w) * (s @ dh + (F + len(ids[m]) + 2) * 2.0 ** -23 * (s @ (np.abs(h) + dh)))
