@@ -11,10 +11,9 @@
 #pragma once
 
 #include "common.hpp"
+#include "mx4_plan.hpp"
 
 namespace w4 {
-
-constexpr int kMxGroup = 32;
 
 struct Mx4Mat {  // [N][K / 2] codes, [N][K / 32] scale bytes, of one matrix or of a stack of them
     const uint8_t* codes;
@@ -63,8 +62,7 @@ __device__ __forceinline__ void store_pieces(uint16_t* row, int64_t k, float v) 
 inline bool launchable(int64_t blocks, int threads) { return blocks <= 0xffffffffLL / threads; }
 
 // More LDS than the default 64 KiB for a kernel with static arrays of up to 16 KiB and `bytes` of dynamic LDS, up to
-// `most` of them; asked for once on each device.
-constexpr int kMostLds = 144 << 10;  // beside such static arrays
+// `most` of them (kMostLds beside such arrays); asked for once on each device.
 template <typename F>
 inline hipError_t allow_lds(F* kern, int bytes, int most, uint64_t* asked) {
     if (bytes <= (48 << 10)) return hipSuccess;

@@ -50,7 +50,7 @@ __device__ __forceinline__ void loads_done_barrier() {
 
 __device__ const __align__(16) uint16_t kMx4Zeros[8] = {};
 
-constexpr int kBlockK = 64, kStages = 4;
+constexpr int kStages = 4;
 template <int BM, int BN, bool PIECES = false>
 constexpr int mx4_stage_bytes() { return BM * kBlockK * 2 + BN * kBlockK / (PIECES ? 4 : 2); }
 

@@ -16,7 +16,6 @@ namespace w4 {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kBlockK4 = 128;
 template <int BM, int BN>
 constexpr int mx4_stage_bytes_x4() { return (BM + BN) * kBlockK4 / 2; }
 

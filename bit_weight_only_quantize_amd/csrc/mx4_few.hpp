@@ -19,12 +19,6 @@
 
 namespace w4 {
 
-constexpr int kFewK = 256;  // k of a step
-
-// bytes of one row of X of `steps` steps in LDS
-__host__ __device__ inline int few_row_bytes(int steps) { return 2 * kFewK * steps + 16; }
-__host__ __device__ inline int few_steps(int64_t K) { return (int)((K + kFewK - 1) / kFewK); }
-
 // Stages steps s0 .. s0 + steps - 1 of `rows` rows, by all threads of the workgroup. row(r): the row's values.
 template <typename Row>
 __device__ __forceinline__ void few_stage(uint8_t* lds, Row row, int rows, int K, int s0, int steps) {

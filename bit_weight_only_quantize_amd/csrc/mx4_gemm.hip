@@ -310,59 +310,6 @@ static hipError_t launch_block(BlockArgs a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Which block, and in how many pieces of K: the least estimated time. A workgroup's time is its
-// steps times the step's measured time with all slots taken (us; 4096 x 12288 rows, K = 4096: 330 us
-// with 256 x 256, 361, 385, 395 and 512 with the others, in this order; 256 x 128 takes 400 and
-// never wins), plus its start and end;
-// rounds of workgroups follow one another. Pieces cost a launch and their sums' way through
-// memory (2048 x 11008 in 344 blocks of 256 x 256 on 256 slots takes 192 us, in 464 of 256 x 192 171).
-struct BlockShape {
-    int bm, bn, slots;  // slots: workgroups that the GPU holds at once
-    double step, head;
-};
-static const BlockShape kShapes[] = {
-    {256, 256, 256, 1.60, 6}, {256, 192, 256, 1.33, 6}, {0, 0, 0, 0, 0}, {128, 256, 256, 0.98, 5},
-    {128, 128, 512, 1.00, 5}, {64, 128, 768, 0.97, 5},
-};
-// 4 bits on both sides: steps of 128 k (4096 x 12288 rows, K = 16384: 560 us with 256 x 192, then 651,
-// 716 and 1093). 128 x 256 takes 731, 256 x 256 needs more registers than there are and takes 632.
-static const BlockShape kShapesX4[] = {
-    {0, 0, 0, 0, 0}, {256, 192, 256, 1.09, 6}, {256, 128, 256, 0.85, 5}, {0, 0, 0, 0, 0},
-    {128, 128, 512, 0.93, 3}, {64, 128, 768, 1.07, 2},
-};
-struct BlockPlan {
-    int shape, parts;
-};
-static size_t part_bytes(const BlockShape& s, int64_t M, int64_t N) {
-    return (size_t)((M + s.bm - 1) / s.bm * s.bm) * ((N + s.bn - 1) / s.bn * s.bn) * 4;
-}
-static BlockPlan block_plan(int64_t M, int64_t N, int64_t K, bool x4, bool can_split) {
-    const BlockShape* shapes = x4 ? kShapesX4 : kShapes;
-    BlockPlan best = {0, 1};
-    double least = 1e30;
-    const int64_t steps = x4 ? (K + kBlockK4 - 1) / kBlockK4 : (K + kBlockK - 1) / kBlockK;
-    for (int i = 0; i < 6; ++i) {
-        const BlockShape& s = shapes[i];
-        if (!s.slots) continue;  // never the best for these operands
-        const int64_t tiles = ((M + s.bm - 1) / s.bm) * ((N + s.bn - 1) / s.bn);
-        for (int p = 1; p <= 16 && 4 * p <= steps + 3; ++p) {
-            if (p > 1 && (!can_split || tiles * p > s.slots)) break;
-            const double rounds = (double)((tiles * p + s.slots - 1) / s.slots);
-            // workgroups that have a CU to themselves take two thirds of the time of two, half that of three
-            const double alone = s.slots > 256 && tiles * p <= 256 ? 0.6 : 1.0;
-            double t = rounds * ((double)((steps + p - 1) / p) * s.step * alone + s.head);
-            if (p > 1) t += 4 + 2.0 * p * part_bytes(s, M, N) / 5e6;
-            if (t < least) {
-                least = t;
-                best = {i, p};
-            }
-        }
-    }
-    return best;
-}
-
-static constexpr int64_t kFewRows = 16;
-
 size_t mx4_gemm_workspace(int64_t M, int64_t N, int64_t K, bool x4) {
     if (M <= kFewRows) return 0;
     const BlockPlan p = block_plan(M, N, K, x4, true);

@@ -24,27 +24,6 @@ struct Mx4MoeWork {  // byte offsets
     size_t tiles, pairs, place, h, part, total;
     int64_t slots;
 };
-struct MoeWay {
-    bool direct;
-    int rows;  // of a tile
-};
-
-constexpr int64_t kDirectPairs = 16;
-
-// Rows of a tile: half a tile an expert is wasted, and the weights are read once a tile. 256 pairs an
-// expert in the mean (32768 over 128, 768 x 2048): gate/up 258 us and down 175 in blocks of 64 x 256, 272
-// and 184 of 128 x 128, whose steps cost less for their size and which win with more pairs.
-static MoeWay moe_way(int64_t M, int k, int64_t E, int64_t D, int64_t F) {
-    const int64_t P = M * k;
-    if (P <= kDirectPairs && k * F <= (32 << 10) && D <= (64 << 10)) return {true, 0};
-    // rows that fit in LDS, of x and of pieces of h
-    const int steps = few_steps(D) > 2 * few_steps(F) ? few_steps(D) : 2 * few_steps(F);
-    const int64_t each = P / E, room = kMostLds / few_row_bytes(steps);
-    if (each <= 6 && room >= 8) return {false, 8};
-    if (each <= 16 && room >= 16) return {false, 16};
-    return {false, each <= 320 ? 64 : 128};
-}
-
 static Mx4MoeWork moe_layout(int64_t M, int k, int64_t E, int64_t D, int64_t F) {
     const int64_t P = M * k;
     const MoeWay way = moe_way(M, k, E, D, F);
