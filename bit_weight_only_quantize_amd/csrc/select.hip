@@ -162,11 +162,14 @@ __device__ void select_exact(const SelectArgs& a, int64_t m, double* values) {
     }
 }
 
-// Errors of the fp32 values. exp2 of y = (l - max) log2 e: y is off by 2^-23 |y|, its power by that times itself and a
-// unit, 2^y (|y| 2^-23 + 2^-23) <= 2^-22; the sum of up to 16 + 6 additions by 22 * 2^-24 of itself: a softmax is
-// within 2^-19 / sum of the true one, its largest. A sigmoid s has s (1 - s) times the power's
+// Errors of the fp32 values, in units u = 2^-23. y = (l - max) log2 e is off by 1.2 u |y|, so the power by
+// 2^y (0.8 |y| + 1) u of its own, at most 1.1 u. Their sum S >= 1 is off by up to (0.8 |y| + 1) u of each summand (5 and 1 u of
+// S at the worst, most of 1024 logits some 8 binades below the largest) and 22 additions (11 u), its reciprocal by half a
+// unit: a factor 1 + d common to all scores, |d| < 18 u. Two scores' difference is then off by d times itself, at most 18 u / S, and by
+// their own errors, 2 (1.1 + 0.5 for the product) u / S: 22 u / S, under the 2 kSoftmaxOff / S = 32 u / S that a decision
+// between two asks for. Sums of two scores: 36 + 7 u / S, under 4 kSoftmaxOff. A sigmoid s has s (1 - s) times the power's
 // relative error, and units for the sum and the reciprocal: within 2^-21. c's rounding: 2^-24 |c|.
-constexpr float kSoftmaxOff = 0x1p-19f, kSigmoidOff = 0x1p-21f;
+constexpr float kSoftmaxOff = 0x1p-19f, kSigmoidOff = 0x1p-21f;  // (the first divided by S)
 
 constexpr int kSelectWaves = 4;
 
