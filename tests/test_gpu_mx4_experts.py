@@ -71,3 +71,32 @@ def test_rows_at_the_ends_of_lds(M, E, k, D, F):
     y = w4.mx4_moe(*(device(c, sc) for c, sc, _ in s), x.cuda(), ids.cuda(), w.cuda(), "silu").cpu().double().numpy()
     want, bound = oracle.mx4_moe(*(v for _, _, v in s), x.double().numpy(), ids.numpy(), w.double().numpy(), "silu")
     assert (np.abs(y - want) <= bound).all()
+
+
+@pytest.mark.parametrize("M", [1, 20, 700])
+def test_the_ends_of_large_stacks(M):
+    """Stacks past 2^32 code bytes, zero but for the last expert's last rows; tolerances of what is rounded: gate and up, sums of
+    96 products that are not zero (2^-23 each), the activation (slope under 1.13, 2^-18 of itself and 2^-22 |g u|), h to 16 bits, y
+    to bf16."""
+    E, F, D = 70, 2048, 65536
+    q = [w4.empty_quantized("mx4_g32", *s, num_experts=E) for s in ((F, D), (F, D), (D, F))]
+    for m in q:
+        m.codes.zero_()
+        m.scale.fill_(127)
+    gc, gs, gv = integers((2, D), 1, 120, 121)
+    for m in q[:2]:
+        m.codes[E - 1, F - 2:] = torch.from_numpy(gc).cuda()
+        m.scale[E - 1, F - 2:] = torch.from_numpy(gs).cuda()
+    q[2].codes[E - 1, D - 1, F // 2 - 1] = 0x22          # 1 times the last two h
+    x = torch.zeros((M, D), dtype=torch.bfloat16)
+    x[:, :96] = torch.randn((M, 96), generator=torch.Generator().manual_seed(M)).to(torch.bfloat16)
+    ids = torch.full((M, 2), E - 1, dtype=torch.int32)
+    y = w4.mx4_moe(*q, x.cuda(), ids.cuda(), torch.full((M, 2), 0.5).cuda()).cpu().double()
+    xv = x[:, :96].double().numpy()
+    g = xv @ gv[:, :96].T
+    off = 96 * 2.0 ** -23 * (np.abs(xv) @ np.abs(gv[:, :96].T))
+    h = oracle.gated(g, g, "gelu_tanh")
+    dh = 1.13 * off * (np.abs(g) + off) + np.abs(g) * off + 2.0 ** -18 * np.abs(h) + 2.0 ** -22 * g * g + 2.0 ** -16 * np.abs(h)
+    want, bound = h.sum(1), (dh + 2.0 ** -21 * np.abs(h)).sum(1)
+    assert (np.abs(y[:, D - 1].numpy() - want) <= bound + 2.0 ** -8 * (np.abs(want) + bound)).all()
+    assert not bool(y[:, :D - 1].any())
