@@ -69,10 +69,10 @@ extern "C" {
  * A quantized matrix, or a stack of `num_experts` matrices of identical shape
  * stored back to back at a fixed stride ([TurboFieldfare]: 128 fixed-stride expert
  * blobs per layer). All three arrays are [num_experts][N][...] as described above.
- * `bias` is NULL for W4_SYM4_G128 and required otherwise.
+ * `bias` is NULL for W4_SYM4_G128 and W4_MX4_G32 and required otherwise.
  */
 typedef struct w4_matrix {
-    int32_t scheme;      /* W4_SYM4_G128, W4_AFF4_G64 or W4_AFF8_G64 */
+    int32_t scheme;      /* one of the above */
     int32_t num_experts; /* >= 1 */
     int64_t N;           /* rows per matrix (output features) */
     int64_t K;           /* columns (input features) */
@@ -603,7 +603,7 @@ int w4_kv_attention(const w4_kv_pages* cache, const w4_kv_batch* batch, const w4
 int w4_mx4_quantize(const w4_rows* x, int64_t rows, int64_t K, void* codes, void* scale, void* stream);
 
 /* The values of q (one matrix) to out [N][K], fp32 or bf16 (exact in both, but for
- * bf16 numbers under 2^-133), a multiple of 16 bytes from row to row. */
+ * bf16 numbers under 2^-133, and infinite from 2^128 on), a multiple of 16 bytes from row to row. */
 int w4_mx4_read(const w4_matrix* q, const w4_rows* out, void* stream);
 
 /*
@@ -613,7 +613,9 @@ int w4_mx4_read(const w4_matrix* q, const w4_rows* out, void* stream);
  * Y: fp32 or bf16 (nearest even), Y's row_stride >= N. Products are exact and sums
  * fp32; a row of X with an infinity or NaN gives what the sum gives, a NaN scale
  * NaN. With bf16 X, numbers under 2^-126 (of X, or a code times its scale) may count
- * as 0. W: one matrix; M (up to 2^26) and N may be 0. Any number of
+ * as 0, and a code times its scale from 2^128 on (scale bytes 253 and 254, which
+ * quantization never writes) is infinite, so that Y's column of its row of W is
+ * infinite or NaN; with X in 4 bits such weights are as exact as others. W: one matrix; M (up to 2^26) and N may be 0. Any number of
  * rows takes the same call: few rows stream the weights, many fill matrix tiles.
  * workspace: w4_mx4_gemm_workspace_bytes(...) bytes (x4: whether X is quantized), 0 for
  * most sizes; contents on entry do not matter. Without it (NULL and 0 bytes) the
@@ -666,7 +668,7 @@ int w4_moe_select(const w4_rows* logits, int64_t M, int64_t E, const w4_select* 
  * [E][F][D]; down [E][D][F]; D and F multiples of 32. x bf16 [M][D]; y bf16 [M][D] with a
  * row stride >= D, not overlapping x. ids, weights [M][top_k] as w4_moe_select or w4_moe_route give them;
  * a slot whose id lies outside [0, E) contributes nothing, and a token without any gets
- * y = 0. An expert's weights are read once for a tile of its tokens (8 to 128,
+ * y = 0. Weights from 2^128 on are infinite, as above. An expert's weights are read once for a tile of its tokens (8 to 128,
  * by how many an expert gets). Sums are fp32, h is kept to 16 bits (two bf16 numbers). 0 <= M, M * top_k <= 2^24, top_k <= 32,
  * E <= 1024. workspace: w4_mx4_moe_workspace_bytes(...) bytes; its contents on entry do not
  * matter. Calls sharing a workspace must not overlap. Deterministic.

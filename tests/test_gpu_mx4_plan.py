@@ -65,3 +65,28 @@ def test_experts_in_every_way(case, skewed):
     assert (np.abs(got[:, :D] - want) <= bound).all() and (got[:, D:] == -5).all()
     if M > 3:
         assert not got[3, :D].any()
+
+
+@pytest.mark.parametrize("x4", [False, True])
+@pytest.mark.parametrize("M", [1, 6, 40, 300])
+def test_weights_past_the_range_of_bf16(M, x4):
+    """Codes 4 and 6 at scale byte 253, and 2 to 6 at 254, are 2^128 and more: infinite beside bf16 X, so that their column of Y is
+    infinite or NaN and no other one is touched; exact beside 4 bits. Smaller codes there are like any others. K ends inside a step."""
+    N, K = 70, 224
+    W, wv = random_matrix(N, K, 1)
+    X, xv = random_matrix(M, K, 2)
+    W.scale[:8, 3], X.scale[:, 3] = 127, 40              # 2^-87
+    wide = torch.tensor([4, 6, 2, 3, 4, 6, 1.5, 0.5], dtype=torch.float64)
+    at = torch.tensor([253, 253, 254, 254, 254, 254, 254, 253], dtype=torch.uint8)
+    W.scale[:8, 3] = at.cuda()
+    W.codes[:8, 48:64] = 0
+    W.codes[:8, 50] = torch.tensor([(GRID[:8] == v).nonzero().item() for v in wide], dtype=torch.uint8).cuda()
+    wv[:8, 96:128] = 0
+    wv[:8, 100] = (wide * torch.pow(2.0, at.double() - 127)).cuda()
+    xv[:, 96:128] *= torch.pow(2.0, 40 - 127.0 - (random_matrix(M, K, 2)[0].scale[:, 3:4].double() - 127))
+    want = xv @ wv.t().contiguous()
+    y = w4.mx4_gemm(W, X if x4 else xv.to(torch.bfloat16), dtype=torch.float32).double()
+    first = 0 if x4 else 6
+    assert bool(((y[:, first:] - want[:, first:]).abs() <= K * 2.0 ** -23 * (xv.abs() @ wv[first:].abs().t().contiguous())).all())
+    if not x4:
+        assert not bool(y[:, :6].isfinite().any())
