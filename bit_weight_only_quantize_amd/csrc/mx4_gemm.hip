@@ -43,8 +43,8 @@ static hipError_t launch_gemv1(const Mx4Mat& W, const uint16_t* x, void* Y, bool
 // ---- up to 16 rows of bf16 (mx4_few.hpp): one workgroup of 16 wavefronts a CU owns consecutive
 // tiles of 16 rows of W, `side` of them at a time with 16 / side wavefronts on each one's steps
 // (their sums meet in LDS, in a fixed order), over X staged `chunk` steps at a time. One step of codes in
-// flight a wavefront: 13.7 us for 13 rows, 5120 -> 13824 (14.8 with up to four tiles side by side; 15.5 and 15.9 with
-// two and three steps in flight). 80 us (5.1 TB/s) for 2 rows, 5120 -> 152064.
+// flight a wavefront: 12.8 us for 13 rows, 5120 -> 13824 (with loads of half lines, at 13.7 then: 14.8 with up to four tiles side by
+// side, 15.5 and 15.9 with two and three steps in flight). 80 us (5.1 TB/s) for 2 rows, 5120 -> 152064.
 constexpr int kFewWaves = 16;
 
 __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4Mat W, Mx4X X, int M, void* __restrict__ Y,

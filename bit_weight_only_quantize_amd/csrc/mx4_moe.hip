@@ -200,7 +200,7 @@ __device__ __forceinline__ int4 moe_tile(const int4* tiles, int nb, int& block) 
 
 // ---------------------------------------------------------------- tiles of up to 16 rows
 // Wavefront w takes 16 gate rows and the same 16 up rows (or 16 down rows) and all of K. 61 tokens over 128
-// experts of 768 x 2048, top 8: gate/up 73 us (209 MB; 2, 6 or 8 wavefronts 75 to 81), down 25 (105 MB).
+// experts of 768 x 2048, top 8: gate/up 73 us (209 MB; 2, 6 or 8 wavefronts 75 to 81), down 29 (105 MB; 25 with one piece of h).
 template <bool GU, int NW>
 __global__ __launch_bounds__(64 * NW) void mx4_moe_few_kernel(Mx4Moe a, const int4* __restrict__ tiles,
                                                               const int32_t* __restrict__ pairs, uint16_t* h,

@@ -78,9 +78,16 @@ struct MoeWay {
 
 constexpr int64_t kDirectPairs = 16;
 
-// Rows of a tile: half a tile an expert is wasted, and the weights are read once a tile. 256 pairs an
-// expert in the mean (32768 over 128, 768 x 2048): gate/up 258 us and down 175 in blocks of 64 x 256, 272
-// and 184 of 128 x 128, whose steps cost less for their size and which win with more pairs.
+// Rows of a tile: half a tile an expert is wasted, and the weights are read once a tile. Blocks of 64 x 256
+// against 128 x 128, whose steps cost less for their size and which waste more (us a call, F x D):
+//   pairs an expert     256           384           512
+//   128 x (768 x 2048)  597 and 650   845 and 889   1087 and 1151
+//   60 x (1408 x 2048)  515 and 516   726 and 736   917 and 922
+//   8 x (1408 x 4096)   152 and 165   214 and 196   269 and 251
+//   32 x (1408 x 4096)  534 and 522   735 and 718   927 and 912
+//   8 x (8192 x 4096)                 1153 and 988  1462 and 1237
+// The larger blocks win with long sums, by up to 15%, and lose up to 6% with short ones; with 256 pairs and less they lose in more
+// of these than they win.
 inline MoeWay moe_way(int64_t M, int k, int64_t E, int64_t D, int64_t F) {
     const int64_t P = M * k;
     if (P <= kDirectPairs && k * F <= (32 << 10) && D <= (64 << 10)) return {true, 0};

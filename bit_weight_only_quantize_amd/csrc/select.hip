@@ -10,7 +10,7 @@
 // Sorting is k rounds of a wave-wide maximum over 32-bit keys; a lane holds consecutive experts, so the
 // first lane with the maximum has the lowest index. Bound by its dependent steps and instruction issue (920 vector
 // instructions a token): 8192 tokens, 256 experts in
-// 8 groups, top 8, sigmoid with bias: 18 us (27 with everything in 64 bits; 1.7 for the bytes). Finding the k-th key bit by
+// 8 groups, top 8, sigmoid with bias: 18 to 20 us (27 with everything in 64 bits; 1.7 for the bytes). Finding the k-th key bit by
 // bit with ballots instead of the rounds, and ranking what it leaves, took 26.
 #include "mx4.hpp"
 #include "topk.hpp"

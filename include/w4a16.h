@@ -618,7 +618,7 @@ int w4_mx4_read(const w4_matrix* q, const w4_rows* out, void* stream);
  * infinite or NaN; with X in 4 bits such weights are as exact as others. W: one matrix; M (up to 2^26) and N may be 0. Any number of
  * rows takes the same call: few rows stream the weights, many fill matrix tiles.
  * workspace: w4_mx4_gemm_workspace_bytes(...) bytes (x4: whether X is quantized), 0 for
- * most sizes; contents on entry do not matter. Without it (NULL and 0 bytes) the
+ * most sizes (fewer rows may need more than many); contents on entry do not matter. Without it (NULL and 0 bytes) the
  * product takes fewer workgroups and longer. Calls sharing a workspace must not
  * overlap. Y must not overlap the inputs. Deterministic;
  * the order of sums depends on the sizes, and on whether there is a workspace.
