@@ -91,7 +91,8 @@ constexpr int64_t kDirectPairs = 16;
 inline MoeWay moe_way(int64_t M, int k, int64_t E, int64_t D, int64_t F) {
     const int64_t P = M * k;
     if (P <= kDirectPairs && k * F <= (32 << 10) && D <= (64 << 10)) return {true, 0};
-    // rows that fit in LDS, of x and of pieces of h
+    // rows that fit in LDS, of x and of pieces of h. (h a part at a time instead: 50 tokens, 8 experts of 4096 x 2048, top 2, 94 us
+    // against 98 in blocks, but 16 tokens over 8192 x 4096 247 against 199.)
     const int steps = few_steps(D) > 2 * few_steps(F) ? few_steps(D) : 2 * few_steps(F);
     const int64_t each = P / E, room = kMostLds / few_row_bytes(steps);
     if (each <= 6 && room >= 8) return {false, 8};

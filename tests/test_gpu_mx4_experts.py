@@ -59,10 +59,11 @@ def test_h_is_kept_to_16_bits(M, E, k, D, F, act):
 
 @pytest.mark.parametrize("M,E,k,D,F", [(20, 16, 2, 64, 4352), (20, 16, 2, 64, 4384), (20, 16, 2, 8960, 64), (20, 16, 2, 8992, 64),
                                        (50, 8, 2, 64, 2048), (50, 8, 2, 64, 2080), (50, 8, 2, 4352, 32), (30, 4, 2, 608, 288),
-                                       (1, 4, 8, 64, 4096), (1, 4, 8, 64, 4128)])
+                                       (1, 4, 8, 64, 4096), (1, 4, 8, 64, 4128), (20, 16, 2, 64, 8960), (20, 16, 2, 64, 8992),
+                                       (50, 8, 2, 64, 4352), (50, 8, 2, 64, 4384), (20, 16, 2, 96, 8480)])
 def test_rows_at_the_ends_of_lds(M, E, k, D, F):
-    """The longest rows of x, and of both pieces of h, that tiles of 8 and 16 rows and single tokens hold in LDS, and
-    the next longer ones, which take another way."""
+    """The longest rows of x, and of both pieces of h, that tiles of 8 and 16 rows and single tokens hold
+    in LDS, and the next longer ones, which take another way."""
     s = [matrix((E,) + z, M + i, std=1 / z[1] ** 0.5) for i, z in enumerate(((F, D), (F, D), (D, F)))]
     g = torch.Generator().manual_seed(F)
     x = torch.randn((M, D), generator=g).to(torch.bfloat16)
